@@ -362,6 +362,136 @@ svdq_status svdq_linear_forward_noalloc(const svdq_layer* layer, const uint16_t*
 svdq_status svdq_linear_forward_unfused(const svdq_layer* layer, const uint16_t* X, int32_t M, uint16_t* Y,
                                         void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------- the operators around the layer -------------------- */
+
+/* What a transformer block runs between its linears, in the order in which
+ * each reads what the one before wrote: residual sum + norm + 8-bit output,
+ * the FP8 linear, rotary positions, attention.  Values are bf16 or fp16 (one
+ * type per call), strides are in elements, and innermost dimensions are
+ * contiguous.  Sums, norms and softmax statistics are held in fp32. */
+typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_FP16 = 1 } svdq_dtype;
+
+/* Columns that share one fp32 scale of an FP8 (OCP E4M3) operand. */
+#define SVDQ_FP8_BLOCK 128
+
+/* h = x + residual; y = h / sqrt(mean_k h^2 + eps) * weight;
+ * for each block of 128 columns of a row (the last may be shorter)
+ *   s = max |y| / 448,  q = e4m3(y / s), round to nearest even.
+ * The norm and y are taken from the fp32 sum, not from h as stored.  A block
+ * whose s is below 2^-126 gets s = 0 and zero codes.  A block that holds a
+ * NaN gets s = NaN, zero codes for its finite values and NaN codes (0x7F) for
+ * the rest; an infinity anywhere in a row makes the row's norm infinite, so
+ * the other values of the row become 0.  (|h| above about 1e19 overflows the
+ * fp32 sum of squares in the same way.)
+ * x, residual, h: device [M, K] with row strides (multiples of 8 elements, at
+ * least K); residual may be NULL (h = x) and so may h (not stored).  h may be
+ * x or residual itself.  weight: device [K].  q: device [M, K] bytes, s:
+ * device [M, ceil(K / 128)], both contiguous: the operand of
+ * svdq_fp8_linear where K % 128 == 0.
+ * 1 <= M <= 2^20, 8 <= K <= 65536, K % 8 == 0; eps >= 0 and finite.
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; s: 4 bytes), UNSUPPORTED, DEVICE. */
+svdq_status svdq_add_rmsnorm_quantize(const uint16_t* x, int64_t x_stride, const uint16_t* residual,
+                                      int64_t residual_stride, const uint16_t* weight, float eps, int32_t M,
+                                      int32_t K, int32_t dtype, uint16_t* h, int64_t h_stride, uint8_t* q, float* s,
+                                      void* stream);
+
+/* Y[m, n] = sum over blocks b of 128 along K of
+ *             xs[m, b] ws[n / 128, b] sum_{k in b} xq[m, k] wq[n, k]   + bias[n].
+ * xq: device [M, K] E4M3 codes, xs: device [M, K/128] fp32 (as
+ * svdq_add_rmsnorm_quantize writes them); wq: device [N, K] E4M3 codes, ws:
+ * device [ceil(N / 128), K / 128] fp32 (128 x 128 blocks); bias: device [N]
+ * or NULL; Y: device [M, N].  bias and Y are of `dtype`; all contiguous.
+ * Block sums are formed by the matrix units in fp32, scaled and added in
+ * fp32, rounded once on the store.
+ * The layer's shape rules hold for M, K and N (K % 128 == 0, N % 16 == 0).
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; xs, ws: 4 bytes), UNSUPPORTED, DEVICE. */
+svdq_status svdq_fp8_linear(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                            const uint16_t* bias, int32_t M, int32_t K, int32_t N, int32_t dtype, uint16_t* Y,
+                            void* stream);
+
+#define SVDQ_ROPE_MAX_AXES 8
+
+/* Frequencies of rotary positions with several axes.  Axis a owns dims[a] / 2
+ * consecutive pairs of a head; pair j turns by theta^-e radians per unit of
+ * its axis' position, with e = 2 i / dims[a], i counting the axis' own pairs,
+ * or with `shared` != 0 one ladder through all pairs, e = 2 j / sum(dims).
+ * Writes, for all sum(dims) / 2 pairs, turns[2 j] + turns[2 j + 1] =
+ * theta^-e / (2 pi) as an fp32 value and its remainder, and axis[j].
+ * dims, turns, axis: host.  Errors: ARG (NULL, theta not finite or not
+ * positive), SHAPE (axes outside 1..SVDQ_ROPE_MAX_AXES, an odd or negative
+ * dims[a], sum(dims) not a multiple of 16 or outside 16..512). */
+svdq_status svdq_rope_frequencies(int32_t axes, const int32_t* dims, double theta, int32_t shared, float* turns,
+                                  int32_t* axis);
+
+typedef struct svdq_rope_args {
+  int32_t M;                    /* tokens, 1..2^20 */
+  int32_t axes;                 /* position numbers per token, 1..SVDQ_ROPE_MAX_AXES */
+  int32_t pairs;                /* rotated pairs of a head: a multiple of 8, 2 pairs <= head_dim */
+  int32_t head_dim;             /* a multiple of 8, at most 512 */
+  int32_t interleaved;          /* nonzero: pair j is elements (2 j, 2 j + 1); 0: (j, j + pairs) */
+  int32_t dtype;
+  const int32_t* positions;     /* device [M, axes], |position| < 2^24 */
+  const float*   turns;         /* device [pairs, 2] (svdq_rope_frequencies) */
+  const int32_t* axis;          /* device [pairs], each in 0..axes-1 */
+  /* two groups of heads turned by the same angles (queries and keys); the
+   * second may be absent (heads[1] == 0).  x, y: device, element (m, h, d) at
+   * m * token + h * head + d; strides are multiples of 8 elements. */
+  const uint16_t* x[2];
+  uint16_t* y[2];
+  int32_t heads[2];             /* heads[0] >= 1, heads[0] + heads[1] <= 65536 */
+  int64_t x_token[2], x_head[2], y_token[2], y_head[2];
+} svdq_rope_args;
+
+/* Turns each pair (a, b) of every head of token m by t = 2 pi f_j p, f_j its
+ * frequency in turns and p = positions[m, axis[j]]:
+ *   a' = a cos t - b sin t,  b' = a sin t + b cos t.
+ * p f_j is reduced to a fraction of a turn before it is rounded, so large
+ * positions keep their accuracy.  Elements from 2 * pairs on are copied.  y
+ * may be x with the same strides (in place); other overlap is not allowed.
+ * A value of axis[] outside 0..axes-1 counts as 0.
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; positions, turns, axis: 4), UNSUPPORTED, DEVICE. */
+svdq_status svdq_rope(const svdq_rope_args* args, void* stream);
+
+#define SVDQ_ATTENTION_MAX_HEAD_DIM 128
+
+typedef struct svdq_attention_args {
+  int32_t B;                    /* batch entries, >= 1 */
+  int32_t Sq, Skv;              /* queries (>= 1) and keys (>= 0) per entry, at most 2^24 */
+  int32_t Hq, Hkv;              /* heads; Hq % Hkv == 0, query head h reads K/V head h / (Hq / Hkv) */
+  int32_t D;                    /* head dimension: a multiple of 8, 8..SVDQ_ATTENTION_MAX_HEAD_DIM */
+  int32_t dtype;
+  int32_t causal;               /* nonzero: keys past the query's position are hidden */
+  float scale;                  /* of q . k */
+  float softcap;                /* > 0: scores become softcap * tanh(score / softcap); 0: off */
+  /* device, element (b, i, h, d) at b * batch + i * token + h * head + d;
+   * strides are multiples of 8 elements.  k and v may be NULL if Skv == 0. */
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  int64_t q_batch, q_token, q_head, k_batch, k_token, k_head, v_batch, v_token, v_head, o_batch, o_token, o_head;
+  const float*   slopes;        /* device [Hq] or NULL: adds -slopes[h] * |position(i) - j| to the score */
+  const int32_t* kv_len;        /* device [B] or NULL: keys in use (clamped to 0..Skv); NULL: Skv */
+  const int32_t* prefix;        /* device [B] or NULL: with causal, keys below prefix[b] are visible to all */
+  const int32_t* q_doc;         /* device [B, Sq] or NULL */
+  const int32_t* k_doc;         /* device [B, Skv], given exactly when q_doc is: only equal numbers see each other */
+} svdq_attention_args;
+
+/* O = softmax(scores) V over the visible keys.  The queries are the last Sq
+ * positions in use: position(i) = n - Sq + i with n = kv_len[b].  Key j is
+ * visible to query i if j < n, and (not causal, or j <= position(i), or
+ * j < prefix[b]), and q_doc[i] == k_doc[j].  score = scale q.k, then the cap,
+ * then the distance bias.  A query that sees no key gets zeros.  What K and V
+ * hold at keys that a query does not see (infinities and NaN too) does not
+ * reach its output, and keys from n on are not read as values at all.
+ * Scores and sums are fp32; the weights exp(score - max) are rounded to the
+ * call's type for the product with V and their sum is taken from the rounded
+ * weights.  The same call on the same inputs gives the same bits.
+ * ws: device, 256-byte aligned, svdq_attention_workspace_bytes() bytes, or
+ * NULL if that is 0; calls that overlap in time need one each.
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; slopes, kv_len, prefix, docs: 4),
+ * WORKSPACE, UNSUPPORTED, DEVICE. */
+size_t svdq_attention_workspace_bytes(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_t D);
+svdq_status svdq_attention(const svdq_attention_args* args, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------ misc ---------------------------------- */
 
 const char* svdq_status_str(svdq_status s);

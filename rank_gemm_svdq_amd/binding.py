@@ -19,6 +19,8 @@ __all__ = [
     "quantize_lora_down", "gemm_lora_up", "linear_forward", "linear_forward_unfused", "linear_forward_noalloc",
     "NOALLOC_MAX_WORKSPACE", "fmt_code", "LIB_PATH",
     "ABI_VERSION", "mfma_rate_probe", "reservoir_select", "smooth_candidates", "search_workspace_bytes", "smooth_search", "SearchOpts", "SearchResult",
+    "add_rmsnorm_quantize", "fp8_linear", "rope_frequencies", "RopePlan", "rope", "attention",
+    "attention_workspace", "attention_workspace_bytes", "FP8_BLOCK", "ROPE_MAX_AXES", "ATTENTION_MAX_HEAD_DIM",
 ]
 
 INT4 = 0
@@ -106,6 +108,21 @@ class SearchResult(C.Structure):
                 ("errors", C.c_void_p), ("best_iter", C.c_int32)]
 
 
+class RopeArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("M", "axes", "pairs", "head_dim", "interleaved", "dtype")]
+                + [(n, C.c_void_p) for n in ("positions", "turns", "axis")]
+                + [("x", C.c_void_p * 2), ("y", C.c_void_p * 2), ("heads", C.c_int32 * 2)]
+                + [(n, C.c_int64 * 2) for n in ("x_token", "x_head", "y_token", "y_head")])
+
+
+class AttentionArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("B", "Sq", "Skv", "Hq", "Hkv", "D", "dtype", "causal")]
+                + [("scale", C.c_float), ("softcap", C.c_float)]
+                + [(n, C.c_void_p) for n in "qkvo"]
+                + [(f"{t}_{n}", C.c_int64) for t in "qkvo" for n in ("batch", "token", "head")]
+                + [(n, C.c_void_p) for n in ("slopes", "kv_len", "prefix", "q_doc", "k_doc")])
+
+
 _lib = None
 ABI_VERSION = 8   # SVDQ_ABI_VERSION of include/svdq.h that these structures mirror
 
@@ -149,11 +166,20 @@ def lib():
     L.svdq_search_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     L.svdq_smooth_search.argtypes = [vp, i32, i32, i32, i32, vp, i32, C.POINTER(SearchOpts), vp, sz, vp,
                                      C.POINTER(SearchResult), C.POINTER(Prepared)]
+    L.svdq_add_rmsnorm_quantize.argtypes = [vp, C.c_int64, vp, C.c_int64, vp, C.c_float, i32, i32, i32, vp, C.c_int64,
+                                            vp, vp, vp]
+    L.svdq_fp8_linear.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    L.svdq_rope_frequencies.argtypes = [i32, vp, C.c_double, i32, vp, vp]
+    L.svdq_rope.argtypes = [C.POINTER(RopeArgs), vp]
+    L.svdq_attention_workspace_bytes.restype = sz
+    L.svdq_attention_workspace_bytes.argtypes = [i32] * 6
+    L.svdq_attention.argtypes = [C.POINTER(AttentionArgs), vp, sz, vp]
     for name in ("svdq_device_check", "svdq_layer_sizes", "svdq_workspace_layout", "svdq_calib_absmax",
                  "svdq_pack_host", "svdq_prepare", "svdq_attach_lora", "svdq_kernel_layout",
                  "svdq_unpack_activations", "svdq_quantize_lora_down", "svdq_gemm_lora_up",
                  "svdq_linear_forward", "svdq_linear_forward_unfused", "svdq_linear_forward_noalloc",
-                 "svdq_smooth_search"):
+                 "svdq_smooth_search", "svdq_add_rmsnorm_quantize", "svdq_fp8_linear", "svdq_rope_frequencies",
+                 "svdq_rope", "svdq_attention"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -505,3 +531,224 @@ def reservoir_select(n_calls, k, seed):
     if n < 0:
         raise SvdqError(1, "svdq_reservoir_select")
     return out[:n].tolist()
+
+
+# ------------------------------------------- the operators around the layer
+
+FP8_BLOCK = 128                 # SVDQ_FP8_BLOCK
+ROPE_MAX_AXES = 8               # SVDQ_ROPE_MAX_AXES
+ATTENTION_MAX_HEAD_DIM = 128    # SVDQ_ATTENTION_MAX_HEAD_DIM
+_VALUE_TYPES = None             # torch dtype -> svdq_dtype, made on first use
+
+
+def _value_type(t, what, where):
+    """svdq_dtype of a tensor; bf16 bit patterns may come as int16, as in the rest of the binding."""
+    global _VALUE_TYPES
+    if _VALUE_TYPES is None:
+        torch = _torch()
+        _VALUE_TYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 1}
+    code = _VALUE_TYPES.get(t.dtype)
+    if code is None:
+        raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected bfloat16, float16 or int16 (bf16 bits)")
+    return code
+
+
+def _want(t, what, where, dev, shape=None, dtypes=None, contiguous=True):
+    """A GPU tensor on `dev` of this shape (None: any extent) and type."""
+    if t.device != dev:
+        raise SvdqError(1, f"{where}: {what} is on {t.device}, expected {dev}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if shape is not None and t.shape != shape:
+        raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise SvdqError(1, f"{where}: {what} is not contiguous")
+    elif t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise SvdqError(1, f"{where}: the last dimension of {what} is not contiguous")
+    return t.data_ptr()
+
+
+def _on_gpu(t, what, where):
+    if not t.is_cuda:
+        raise SvdqError(1, f"{where}: {what} is not in GPU memory")
+    torch = _torch()
+    if t.device.index != torch.cuda.current_device():
+        raise SvdqError(1, f"{where}: {what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _stream_on(stream, dev):
+    return (_torch().cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _strides(t, extents):
+    """Strides in elements; those of dimensions with one place, which address nothing, as 0."""
+    return [s if n > 1 else 0 for s, n in zip(t.stride(), extents)]
+
+
+def _fp8_types():
+    torch = _torch()
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=None):
+    """svdq_add_rmsnorm_quantize: h = x + residual, y = h / rms(h) * weight,
+    q, s = y in E4M3 with an fp32 scale per 128 columns.  x, residual, h:
+    [M, K] (rows may be strided; h may be x or residual); weight [K];
+    q [M, K] float8_e4m3fn or uint8; s [M, ceil(K / 128)] float32.  Writes q, s
+    and, if given, h."""
+    where = "svdq_add_rmsnorm_quantize"
+    torch = _torch()
+    dev = _on_gpu(x, "x", where)
+    dt = _value_type(x, "x", where)
+    if x.dim() != 2:
+        raise SvdqError(2, f"{where}: x has shape {tuple(x.shape)}, expected (M, K)")
+    M, K = x.shape
+    own = (x.dtype,)
+    xp = _want(x, "x", where, dev, contiguous=False)
+    wp = _want(weight, "weight", where, dev, (K,), own)
+    qp = _want(q, "q", where, dev, (M, K), _fp8_types())
+    sp = _want(s, "s", where, dev, (M, -(-K // FP8_BLOCK)), (torch.float32,))
+    row = lambda t: t.stride(0) if M > 1 else K
+    rp, rs, hp, hs = None, 0, None, 0
+    if residual is not None:
+        rp, rs = _want(residual, "residual", where, dev, (M, K), own, contiguous=False), row(residual)
+    if h is not None:
+        hp, hs = _want(h, "h", where, dev, (M, K), own, contiguous=False), row(h)
+    _check(lib().svdq_add_rmsnorm_quantize(xp, row(x), rp, rs, wp, eps, M, K, dt, hp, hs, qp, sp,
+                                           _stream_on(stream, dev)), where)
+
+
+def fp8_linear(xq, xs, wq, ws, Y, bias=None, stream=None):
+    """svdq_fp8_linear: Y = (xq xs) (wq ws)^T + bias with E4M3 codes xq [M, K],
+    wq [N, K] (float8_e4m3fn or uint8) and fp32 scales xs [M, K / 128],
+    ws [ceil(N / 128), K / 128]; bias [N] has Y's type.  Writes Y [M, N]."""
+    where = "svdq_fp8_linear"
+    f32 = (_torch().float32,)
+    dev = _on_gpu(xq, "xq", where)
+    if xq.dim() != 2 or wq.dim() != 2 or wq.shape[1] != xq.shape[1]:
+        raise SvdqError(2, f"{where}: xq {tuple(xq.shape)} and wq {tuple(wq.shape)}, expected (M, K) and (N, K)")
+    M, K = xq.shape
+    N = wq.shape[0]
+    dt = _value_type(Y, "Y", where)
+    codes = _fp8_types()
+    xp, wp = _want(xq, "xq", where, dev, None, codes), _want(wq, "wq", where, dev, None, codes)
+    sp = _want(xs, "xs", where, dev, (M, K // FP8_BLOCK), f32)
+    tp = _want(ws, "ws", where, dev, (-(-N // FP8_BLOCK), K // FP8_BLOCK), f32)
+    yp = _want(Y, "Y", where, dev, (M, N))
+    bp = None if bias is None else _want(bias, "bias", where, dev, (N,), (Y.dtype,))
+    _check(lib().svdq_fp8_linear(xp, sp, wp, tp, bp, M, K, N, dt, yp, _stream_on(stream, dev)), where)
+
+
+def rope_frequencies(dims, theta=10000.0, shared=False):
+    """svdq_rope_frequencies: (turns [pairs, 2] float32, axis [pairs] int32) for axes of `dims` elements each."""
+    d = np.ascontiguousarray(dims, np.int32)
+    pairs = max(1, int(np.maximum(d, 0).sum()) // 2)
+    turns, axis = np.zeros((pairs, 2), np.float32), np.zeros(pairs, np.int32)
+    _check(lib().svdq_rope_frequencies(d.size, _p(d), float(theta), int(bool(shared)), _p(turns), _p(axis)),
+           "svdq_rope_frequencies")
+    return turns, axis
+
+
+class RopePlan:
+    """The frequencies of a model's rotary positions in device memory.
+
+    dims: how many elements of a head each axis turns (in this order, from
+    the head's first element on).  shared: one ladder of frequencies through
+    all axes instead of one each.  interleaved: pairs are neighbours
+    (2 j, 2 j + 1) instead of half the turned elements apart."""
+
+    def __init__(self, dims, theta=10000.0, shared=False, interleaved=True, device="cuda"):
+        torch = _torch()
+        turns, axis = rope_frequencies(dims, theta, shared)
+        self.axes, self.pairs, self.interleaved = len(dims), axis.size, bool(interleaved)
+        self.turns = torch.from_numpy(turns).to(device)
+        self.axis = torch.from_numpy(axis).to(device)
+
+
+def rope(plan, positions, x, y, x2=None, y2=None, stream=None):
+    """svdq_rope: turns the heads of x into y (and of x2 into y2, the keys
+    beside the queries) by the angles of positions [M, axes] (int32).  x, y
+    [M, heads, head_dim], x2, y2 [M, heads2, head_dim], any token and head
+    strides that are multiples of 8 elements; y may be x."""
+    where = "svdq_rope"
+    dev = _on_gpu(x, "x", where)
+    dt = _value_type(x, "x", where)
+    if x.dim() != 3:
+        raise SvdqError(2, f"{where}: x has shape {tuple(x.shape)}, expected (M, heads, head_dim)")
+    M, H, D = x.shape
+    own = (x.dtype,)
+    i32 = (_torch().int32,)
+    a = RopeArgs(M, plan.axes, plan.pairs, D, int(plan.interleaved), dt,
+                 _want(positions, "positions", where, dev, (M, plan.axes), i32),
+                 _want(plan.turns, "the plan's turns", where, dev), _want(plan.axis, "the plan's axis", where, dev))
+    a.x[0] = _want(x, "x", where, dev, contiguous=False)
+    a.y[0] = _want(y, "y", where, dev, x.shape, own, contiguous=False)
+    a.heads[0] = H
+    a.x_token[0], a.x_head[0] = _strides(x, (M, H))
+    a.y_token[0], a.y_head[0] = _strides(y, (M, H))
+    if (x2 is None) != (y2 is None):
+        raise SvdqError(1, f"{where}: x2 and y2 go together")
+    if x2 is not None:
+        if x2.dim() != 3 or x2.shape[0] != M or x2.shape[2] != D:
+            raise SvdqError(2, f"{where}: x2 has shape {tuple(x2.shape)}, expected ({M}, heads, {D})")
+        H2 = x2.shape[1]
+        a.x[1] = _want(x2, "x2", where, dev, None, own, contiguous=False)
+        a.y[1] = _want(y2, "y2", where, dev, x2.shape, own, contiguous=False)
+        a.heads[1] = H2
+        a.x_token[1], a.x_head[1] = _strides(x2, (M, H2))
+        a.y_token[1], a.y_head[1] = _strides(y2, (M, H2))
+    _check(lib().svdq_rope(C.byref(a), _stream_on(stream, dev)), where)
+
+
+def attention_workspace_bytes(B, Sq, Skv, Hq, Hkv, D):
+    return lib().svdq_attention_workspace_bytes(B, Sq, Skv, Hq, Hkv, D)
+
+
+def attention_workspace(q, k):
+    """Workspace of attention() for queries and keys of these shapes (to be kept between calls)."""
+    torch = _torch()
+    n = attention_workspace_bytes(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3])
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
+def attention(q, k, v, o, ws, scale=None, causal=False, softcap=0.0, slopes=None, kv_len=None, prefix=None,
+              q_doc=None, k_doc=None, stream=None):
+    """svdq_attention: o = softmax(scores) v.  q, o [B, Sq, Hq, D], k, v
+    [B, Skv, Hkv, D], any strides that are multiples of 8 elements (the last
+    dimension contiguous); ws from attention_workspace().  scale: D ** -0.5
+    if None.  slopes [Hq] float32; kv_len, prefix [B], q_doc [B, Sq], k_doc
+    [B, Skv] int32.  The queries are the last Sq of the kv_len keys' positions."""
+    where = "svdq_attention"
+    torch = _torch()
+    dev = _on_gpu(q, "q", where)
+    dt = _value_type(q, "q", where)
+    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+        raise SvdqError(2, f"{where}: q {tuple(q.shape)} and k {tuple(k.shape)}, expected (B, Sq, Hq, D) and "
+                           "(B, Skv, Hkv, D)")
+    B, Sq, Hq, D = q.shape
+    Skv, Hkv = k.shape[1], k.shape[2]
+    own, i32 = (q.dtype,), (torch.int32,)
+    a = AttentionArgs(B, Sq, Skv, Hq, Hkv, D, dt, int(bool(causal)), D ** -0.5 if scale is None else scale, softcap,
+                      _want(q, "q", where, dev, contiguous=False),
+                      _want(k, "k", where, dev, None, own, contiguous=False),
+                      _want(v, "v", where, dev, k.shape, own, contiguous=False),
+                      _want(o, "o", where, dev, q.shape, own, contiguous=False),
+                      *_strides(q, (B, Sq, Hq)), *_strides(k, (B, Skv, Hkv)), *_strides(v, (B, Skv, Hkv)),
+                      *_strides(o, (B, Sq, Hq)))
+    if slopes is not None:
+        a.slopes = _want(slopes, "slopes", where, dev, (Hq,), (torch.float32,))
+    if kv_len is not None:
+        a.kv_len = _want(kv_len, "kv_len", where, dev, (B,), i32)
+    if prefix is not None:
+        a.prefix = _want(prefix, "prefix", where, dev, (B,), i32)
+    if (q_doc is None) != (k_doc is None):
+        raise SvdqError(1, f"{where}: q_doc and k_doc go together")
+    if q_doc is not None:
+        a.q_doc = _want(q_doc, "q_doc", where, dev, (B, Sq), i32)
+        a.k_doc = _want(k_doc, "k_doc", where, dev, (B, Skv), i32)
+    wp, wn = None, 0
+    if ws is not None:
+        wp, wn = _want(ws, "workspace", where, dev, None, (torch.uint8,)), ws.numel()
+    _check(lib().svdq_attention(C.byref(a), wp if wn else None, wn, _stream_on(stream, dev)), where)

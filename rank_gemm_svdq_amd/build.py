@@ -22,7 +22,12 @@ DEVICE_FLAGS = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-ffp-con
 UNITS = [
     ("host_prepare.cpp", ["g++"] + HOST_FLAGS + ["-ffp-contract=off"]),
     ("host_eigen.cpp", ["g++"] + HOST_FLAGS + ["-ffp-contract=fast"]),
+    ("host_block.cpp", ["g++"] + HOST_FLAGS + ["-ffp-contract=off"]),
     ("device_kernels.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_norm.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_fp8.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_rope.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_attention.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_search.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_probe.hip", [HIPCC] + DEVICE_FLAGS),
 ]

@@ -101,6 +101,11 @@ struct CandidateView {
 };
 using Scorer = std::function<svdq_status(const CandidateView&, double* score)>;
 
+// compute units of the current device, and the gfx950 check, both cached per
+// device (device_kernels.hip)
+int device_cus();
+svdq_status device_ok();
+
 // svdq_prepare with an optional scorer of the residual iterations.
 svdq_status prepare_layer(const float* W, const float* act_amax, int32_t K, int32_t N, double alpha, int32_t rank,
                           int32_t fmt, const svdq_prepare_opts* opts, svdq_prepared* out, const Scorer* scorer);
