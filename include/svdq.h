@@ -379,8 +379,8 @@ typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_FP16 = 1 } svdq_dtype;
  *   s = max |y| / 448,  q = e4m3(y / s), round to nearest even.
  * The norm and y are taken from the fp32 sum, not from h as stored.  A block
  * whose s is below 2^-126 gets s = 0 and zero codes.  A block that holds a
- * NaN gets s = NaN, zero codes for its finite values and NaN codes (0x7F) for
- * the rest; an infinity anywhere in a row makes the row's norm infinite, so
+ * NaN gets s = NaN, zero codes for its finite values and NaN codes for the
+ * rest; an infinity anywhere in a row makes the row's norm infinite, so
  * the other values of the row become 0.  (|h| above about 1e19 overflows the
  * fp32 sum of squares in the same way.)
  * x, residual, h: device [M, K] with row strides (multiples of 8 elements, at
@@ -464,7 +464,8 @@ typedef struct svdq_attention_args {
   float scale;                  /* of q . k */
   float softcap;                /* > 0: scores become softcap * tanh(score / softcap); 0: off */
   /* device, element (b, i, h, d) at b * batch + i * token + h * head + d;
-   * strides are multiples of 8 elements.  k and v may be NULL if Skv == 0. */
+   * strides are multiples of 8 elements, k_token and v_token in 0..2^28.  k and
+   * v may be NULL if Skv == 0.  B Hq Sq is at most 2^30. */
   const uint16_t *q, *k, *v;
   uint16_t* o;
   int64_t q_batch, q_token, q_head, k_batch, k_token, k_head, v_batch, v_token, v_head, o_batch, o_token, o_head;
@@ -482,9 +483,9 @@ typedef struct svdq_attention_args {
  * then the distance bias.  A query that sees no key gets zeros.  What K and V
  * hold at keys that a query does not see (infinities and NaN too) does not
  * reach its output, and keys from n on are not read as values at all.
- * Scores and sums are fp32; the weights exp(score - max) are rounded to the
- * call's type for the product with V and their sum is taken from the rounded
- * weights.  The same call on the same inputs gives the same bits.
+ * Scores, the running maximum and sum and O are fp32; the weights
+ * exp(score - max) are rounded to the call's type for the product with V (not
+ * for their sum).  The same call on the same inputs gives the same bits.
  * ws: device, 256-byte aligned, svdq_attention_workspace_bytes() bytes, or
  * NULL if that is 0; calls that overlap in time need one each.
  * Errors: ARG, SHAPE, ALIGN (16 bytes; slopes, kv_len, prefix, docs: 4),

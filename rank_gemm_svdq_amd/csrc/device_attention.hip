@@ -1,54 +1,567 @@
 // Attention over visible keys, with shared K/V heads, score cap, distance
-// bias, document numbers, a prefix and lengths.
+// bias, document numbers, a prefix and lengths: one pass over K and V with the
+// running maximum and sum of the softmax, scores never leave registers.
 //
-// One wave per (entry, head, query): lane l holds elements 2 l, 2 l + 1 of
-// the head, each visible key is one dot product over the wave and one step of
-// the running maximum and sum.
+// Rows.  The queries of all heads that share a K/V head are rows of one
+// matrix: row r is query r / G of head hk G + r % G (G heads share).  A wave
+// owns 32 rows, so one pass over K and V serves all G heads.
+//
+// One tile of 32 keys, per wave (32x32x16 MFMA; lane l: column l % 32,
+// l / 32 = half):
+//   S^T = K Q^T   A = 32 keys (LDS), B = the wave's rows (registers).  Lane l
+//                 gets row l % 32, keys 8 (i / 4) + 4 half + i % 4 in register i.
+//   softmax       a row's 32 scores sit in two lanes (l, l + 32): its maximum
+//                 is a register reduction and one half exchange.
+//   O^T += V^T P  the order of the keys inside an MFMA is free as long as both
+//                 operands agree, and with keys 16 s + 4 half + {0..3, 8..11}
+//                 in the 8 slots of a lane, registers 8 s' .. + 8 of S are the
+//                 B operand as they stand, rounded to 16 bits: P does not
+//                 cross lanes.  A comes from V as it lies in memory by
+//                 transposing LDS reads (4 keys x 16 columns a read).
+// K and V tiles go to LDS by direct copies.  16-byte chunks of a K row are
+// XORed with row bits and 64-byte chunks of a V row likewise, so that the
+// reads above hit all banks evenly (k_chunk, v_chunk).
+//
+// The maximum is raised only when a tile's exceeds it by more than 8 (in
+// powers of two): the weights stay below 2^8 and the rescaling of O is rare.
+//
+// Two arrangements.  More than 32 rows: the four waves of a block take 128
+// rows and share tiles of 64 keys.  At most 32 rows (a few new tokens): the
+// waves share the rows and take tiles of 32 keys in turn, each with its own
+// buffers and no barriers, and are joined at the end.  Where blocks are few,
+// the keys are split over blocks too; a second kernel joins the parts.
+//
+// Hidden keys.  A hidden score is -infinity, its weight 0, and 0 times what V
+// holds there would be NaN if that is not finite.  O is checked at the end:
+// rows that came out not finite are computed again key by key, without the
+// hidden ones (row_again).
 
 #include "device_block.h"
 
 namespace svdq {
 namespace {
 
+constexpr int kCus = 256;   // compute units of the chip, for the host-side choice of splits
+
+struct Part {               // how the keys are split over blocks
+  int32_t splits;
+  float* o;                 // [splits][rows][DP]: sums of weights times values
+  float* ml;                // [splits][rows][2]: maximum (log2) and sum of weights
+};
+
+struct AttnP {
+  svdq_attention_args a;
+  int G, R, tiles, groups;  // heads per K/V head, rows per (entry, K/V head), row tiles, entries x K/V heads
+  float qmul, c1, c2, c3;   // see launch()
+  bool flip;
+  Part part;
+};
+
 template <int DT>
-__global__ __launch_bounds__(256) void attention_row_kernel(svdq_attention_args a) {
+__device__ __forceinline__ b16f mma(const b4i& a, const b4i& b, const b16f& c) {
+  if constexpr (DT == SVDQ_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8bf, a), __builtin_bit_cast(b8bf, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(b8h, a), __builtin_bit_cast(b8h, b), c, 0, 0, 0);
+}
+
+// both halves' value of the lane pair (l, l + 32)
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Score in powers of two of a raw dot product (times scale > 0, cap and bias).
+__device__ __forceinline__ float capped(const AttnP& p, float s) {
+  // cap tanh(s scale / cap) = cap - 2 cap / (e^(2 s scale / cap) + 1), times log2 e
+  return fmaf(-2.0f * p.c3, __builtin_amdgcn_rcpf(exp2_(s * p.c2) + 1.0f), p.c3);
+}
+
+constexpr float kLow = -3.402823466e38f;
+
+// One row key by key over [j0, j1), lane l with elements 2 l, 2 l + 1: the
+// maximum, the sum and the weighted values of the visible keys alone.
+template <int DT>
+__device__ __forceinline__ void row_again(const AttnP& p, int b, int hk, int r, int n, int j0, int j1, float* m_out,
+                                          float* l_out, b2f* o_out) {
+  const svdq_attention_args& a = p.a;
   const int lane = threadIdx.x & 63;
-  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (id >= (int64_t)a.B * a.Hq * a.Sq) return;
-  const int i = (int)(id % a.Sq), h = (int)(id / a.Sq % a.Hq), b = (int)(id / a.Sq / a.Hq);
-  const int hk = h / (a.Hq / a.Hkv);
+  const int i = r / p.G, h = hk * p.G + r % p.G;
   const bool live = 2 * lane < a.D;
-  const int n = a.kv_len ? min(max(a.kv_len[b], 0), a.Skv) : a.Skv;
   const int pos = n - a.Sq + i;
-  const int pre = a.causal && a.prefix ? a.prefix[b] : 0;
-  const int end = a.causal ? min(n, max(pos + 1, pre)) : n;
-  const int doc = a.q_doc ? a.q_doc[(size_t)b * a.Sq + i] : 0;
-  auto pair = [&](const uint16_t* p) { return live ? widen2<DT>(*reinterpret_cast<const uint32_t*>(p + 2 * lane)) : (b2f){0.f, 0.f}; };
+  auto pair = [&](const uint16_t* t) {
+    return live ? widen2<DT>(*reinterpret_cast<const uint32_t*>(t + 2 * lane)) : (b2f){0.f, 0.f};
+  };
   const b2f q = pair(a.q + b * a.q_batch + i * a.q_token + h * a.q_head);
-  float top = -__builtin_inff(), sum = 0.f;
+  const int end = a.causal ? min(j1, max(pos + 1, a.prefix ? a.prefix[b] : 0)) : j1;
+  float top = kLow, sum = 0.f;
   b2f o = (b2f){0.f, 0.f};
-  for (int j = 0; j < end; ++j) {
-    if (a.q_doc && a.k_doc[(size_t)b * a.Skv + j] != doc) continue;
+  for (int j = j0; j < end; ++j) {
+    if (a.q_doc && a.k_doc[(size_t)b * a.Skv + j] != a.q_doc[(size_t)b * a.Sq + i]) continue;
     const b2f k = pair(a.k + b * a.k_batch + j * a.k_token + hk * a.k_head);
     float s = fmaf(q[0], k[0], q[1] * k[1]);
 #pragma unroll
     for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-    s *= a.scale;
-    if (a.softcap > 0.f) s = a.softcap * tanhf(s / a.softcap);
-    if (a.slopes) s -= a.slopes[h] * fabsf((float)(pos - j));
+    s *= p.qmul;
+    s = a.softcap > 0.f ? capped(p, s) : s * p.c1;
+    if (a.slopes) s -= a.slopes[h] * 1.44269504f * fabsf((float)(pos - j));
     const float up = fmaxf(top, s);
-    const float base = up == -__builtin_inff() ? 0.f : up;
-    const float f = __expf(top - base), w = __expf(s - base);
+    const float f = exp2_(top - up), w = exp2_(s - up);
     const b2f v = pair(a.v + b * a.v_batch + j * a.v_token + hk * a.v_head);
     sum = fmaf(sum, f, w);
     o[0] = fmaf(o[0], f, w * v[0]);
     o[1] = fmaf(o[1], f, w * v[1]);
     top = up;
   }
+  *m_out = top;
+  *l_out = sum;
+  *o_out = o;
+}
+
+// KEYS: waves share 32 rows and take key tiles in turn; otherwise waves take
+// rows and share key tiles.  PAD: D < DP.
+template <int DT, int DP, bool PAD, bool KEYS>
+__global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_kernel(AttnP p) {
+  const svdq_attention_args& a = p.a;
+  constexpr int KT = KEYS ? 1 : 2;                 // 32-key subtiles of a tile
+  constexpr int TK = 32 * KT;
+  constexpr int ROWB = 2 * DP;                     // bytes of a row in LDS
+  constexpr int TILE = TK * ROWB;                  // one of K, V
+  constexpr int CH = DP / 8;                       // 16-byte chunks of a row
+  constexpr int RPI = 64 / CH;                     // rows of one 1 KB copy
+  constexpr int COPIES = TILE / 1024;              // of K or V, per tile
+  constexpr int MINE = KEYS ? COPIES : COPIES / 4; // per wave
+  constexpr int NS = DP / 16;                      // MFMA steps of S
+  constexpr int ND = DP / 32;                      // 32-column tiles of O
+  constexpr int RING = 4 * TILE;                   // K, V of two tiles
+  constexpr int LDS = KEYS ? 4 * RING : RING;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
+  __shared__ int docs[4][TK];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, half = lane >> 5;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int per_group = p.tiles * p.part.splits;
+  const int grp = id / per_group, rest = id % per_group;
+  // the last rows see most keys under a causal mask: they go first
+  const int rt = p.tiles - 1 - rest / p.part.splits, sp = rest % p.part.splits;
+  const int b = grp / a.Hkv, hk = grp % a.Hkv;
+  const int n = a.kv_len ? min(max(a.kv_len[b], 0), a.Skv) : a.Skv;
+  const int pre = a.causal && a.prefix ? a.prefix[b] : 0;
+  const int row_base = rt * (KEYS ? 32 : 128);
+  const int row0 = row_base + (KEYS ? 0 : 32 * wave);
+  const int row = min(row0 + l32, p.R - 1);
+  const int qi = row / p.G, qh = hk * p.G + row % p.G;
+  const int pos = n - a.Sq + qi;
+  auto limit = [&](int r) {   // keys below it may be visible to row r
+    return a.causal ? min(n, max(max(n - a.Sq + r / p.G + 1, pre), 0)) : n;
+  };
+  const int lim = limit(row);
+  const int lim_first = limit(min(row0, p.R - 1)), lim_last = limit(min(row0 + 31, p.R - 1));
+  const int end = limit(min(row_base + (KEYS ? 31 : 127), p.R - 1));
+  const bool use_docs = a.q_doc != nullptr;
+  const float slope = a.slopes ? a.slopes[qh] * 1.44269504f : 0.f;
+
+  // this block's tiles
+  const int all = (end + TK - 1) / TK;
+  const int share = (all + p.part.splits - 1) / p.part.splits;
+  const int t_begin = min(all, sp * share), t_end = min(all, t_begin + share);
+
+  // ---- Q as the B operand: step s, elements 16 s + 8 half .. + 8 of the lane's row
+  b4i qf[NS];
+  {
+    const uint16_t* qp = a.q + b * a.q_batch + qi * a.q_token + qh * a.q_head;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int d = 16 * s + 8 * half;
+      qf[s] = (b4i){0, 0, 0, 0};
+      if (!PAD || d < a.D) qf[s] = *reinterpret_cast<const b4i*>(qp + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (p.flip) qf[s][i] ^= (int)0x80008000;
+        if (p.qmul == 0.f) qf[s][i] = 0;
+      }
+    }
+  }
+  const int qd = use_docs ? a.q_doc[(size_t)b * a.Sq + qi] : 0;
+  int doc_lo = 0, doc_hi = 0;   // of the rows of the block (rows arrangement) or the wave
+  if (use_docs) {
+    doc_lo = doc_hi = qd;
+    if constexpr (!KEYS) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int d = a.q_doc[(size_t)b * a.Sq + min(row_base + 64 * k + lane, p.R - 1) / p.G];
+        doc_lo = min(doc_lo, d);
+        doc_hi = max(doc_hi, d);
+      }
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) {
+      doc_lo = min(doc_lo, __shfl_xor(doc_lo, d));
+      doc_hi = max(doc_hi, __shfl_xor(doc_hi, d));
+    }
+  }
+  const int qd_first = __builtin_amdgcn_readfirstlane(qd);
+  const bool one_doc = use_docs && __all(qd == qd_first);
+
+  // ---- copies to LDS
+  const uint32_t lbase = lds_address(lds) + (KEYS ? wave * RING : 0);
+  if constexpr (PAD) {
+    // columns D .. DP of the buffers are never copied: zero for good
+    uint32_t* w = reinterpret_cast<uint32_t*>(lds);
+    for (int i = threadIdx.x; i < LDS / 4; i += 256) w[i] = 0;
+    __syncthreads();
+  }
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(a.k + b * a.k_batch + hk * a.k_head);
+  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(a.v + b * a.v_batch + hk * a.v_head);
+  const int crow = lane / CH, cslot = lane % CH;   // row and 16-byte slot of a copy's lane
+  // chunk of K row r at slot c and the other way round
+  auto k_chunk = [&](int r, int c) { return DP == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7); };
+  auto v_chunk = [&](int r, int c) { return DP == 128 ? c ^ (4 * (r & 3)) : c ^ (4 * ((r >> 1) & 1)); };
+  const uint64_t kst = 2 * (uint64_t)a.k_token, vst = 2 * (uint64_t)a.v_token;
+  auto copy_tile = [&](int t, int buf) __attribute__((always_inline)) {
+    const int j0 = t * TK, last = n - 1 - j0;      // rows past the last key in use repeat it
+#pragma unroll
+    for (int c = 0; c < MINE; ++c) {
+      const int r0 = RPI * (KEYS ? c : MINE * wave + c);
+      const int from = min(r0, last);
+      const uint32_t dr = (uint32_t)(min(r0 + crow, last) - from);
+      const int kc = k_chunk(r0 + crow, cslot);
+      if (!PAD || 8 * kc < a.D)
+        dma_16(kbase + (uint64_t)(j0 + from) * kst, dr * (uint32_t)kst + 16 * kc, lbase + buf * 2 * TILE + RPI * ROWB * (KEYS ? c : MINE * wave + c));
+    }
+#pragma unroll
+    for (int c = 0; c < MINE; ++c) {
+      const int r0 = RPI * (KEYS ? c : MINE * wave + c);
+      const int from = min(r0, last);
+      const uint32_t dr = (uint32_t)(min(r0 + crow, last) - from);
+      const int vc = v_chunk(r0 + crow, cslot);
+      if (!PAD || 8 * vc < a.D)
+        dma_16(vbase + (uint64_t)(j0 + from) * vst, dr * (uint32_t)vst + 16 * vc,
+               lbase + buf * 2 * TILE + TILE + RPI * ROWB * (KEYS ? c : MINE * wave + c));
+    }
+  };
+
+  // fragment addresses
+  const uint8_t* wl = lds + (KEYS ? wave * RING : 0);
+  int koff[NS], voff[ND];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) koff[s] = l32 * ROWB + 16 * k_chunk(l32, 2 * s + half);
+  {
+    const int i16 = lane & 15, dh = (lane >> 4) & 1, kr = 4 * half + i16 / 4;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) voff[d] = kr * ROWB + 16 * v_chunk(kr, 4 * d) + 32 * dh + 8 * (i16 % 4);
+  }
+
+  float m = kLow, l = 0.f;
+  b16f o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+
+  const bool plain = !(a.softcap > 0.f) && !a.slopes;   // score = c1 x dot product
+
+  // kd: document of key j0 + lane (where documents are used)
+  auto compute = [&](int t, int buf, int kd) __attribute__((always_inline)) {
+    const int j0 = t * TK;
+    const uint8_t* kl = wl + buf * 2 * TILE;
+    const uint8_t* vl = kl + TILE;
+    b16f s[KT];
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[k][i] = 0.f;
+#pragma unroll
+      for (int x = 0; x < NS; ++x)
+        s[k] = mma<DT>(*reinterpret_cast<const b4i*>(kl + koff[x] + k * 32 * ROWB), qf[x], s[k]);
+    }
+    float c = p.c1;
+    if (!plain) {
+      c = 1.f;
+      if (a.softcap > 0.f) {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[k][i] = capped(p, s[k][i]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[k][i] *= p.c1;
+      }
+      if (a.slopes) {
+        const float from = (float)(pos - j0 - 4 * half);
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[k][i] = fmaf(-slope, fabsf(from - (float)(32 * k + 8 * (i / 4) + i % 4)), s[k][i]);
+      }
+    }
+    if (j0 + TK > lim_first) {
+      const int rel = lim - j0 - 4 * half;
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (32 * k + 8 * (i / 4) + i % 4 >= rel) s[k][i] = -__builtin_inff();
+    }
+    if (use_docs && !(one_doc && __all(kd == qd_first))) {
+      docs[wave][lane & (TK - 1)] = kd;
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int k = 0; k < KT; ++k)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const b4i kk = *reinterpret_cast<const b4i*>(&docs[wave][32 * k + 8 * g + 4 * half]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (kk[i] != qd) s[k][4 * g + i] = -__builtin_inff();
+        }
+      __builtin_amdgcn_wave_barrier();
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[k][i]);
+    top = half_max(top) * c;
+    if (__any(top > m + 8.0f)) {
+      const float up = fmaxf(m, top);
+      const float f = exp2_(m - up);
+      m = up;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= f;
+    }
+    b4i pf[2 * KT];
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      float part = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[k][i] = exp2_(fmaf(s[k][i], c, -m));
+        part += s[k][i];
+      }
+      l += part;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) pf[2 * k + x / 4][x % 4] = (int)narrow2<DT>(s[k][2 * x], s[k][2 * x + 1]);
+    }
+    typedef short s4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int x = 0; x < 2 * KT; ++x) {
+        const s4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SVDQ_LDS s4*)(vl + voff[d] + 16 * x * ROWB));
+        const s4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SVDQ_LDS s4*)(vl + voff[d] + (16 * x + 8) * ROWB));
+        const int2 lo = __builtin_bit_cast(int2, v0), hi = __builtin_bit_cast(int2, v1);
+        o[d] = mma<DT>((b4i){lo.x, lo.y, hi.x, hi.y}, pf[x], o[d]);
+      }
+  };
+  auto doc_of = [&](int t) -> int {
+    return use_docs && t < t_end ? a.k_doc[(size_t)b * a.Skv + min(t * TK + (lane & (TK - 1)), n - 1)] : 0;
+  };
+
+  if constexpr (KEYS) {
+    // each wave on its own: tiles t_begin + wave, + 4, ...
+    int t = t_begin + wave, buf = 0;
+    if (t < t_end) copy_tile(t, 0);
+    int kd = doc_of(t);
+    for (; t < t_end; t += 4, buf ^= 1) {
+      dma_wait();
+      __builtin_amdgcn_wave_barrier();
+      if (t + 4 < t_end) copy_tile(t + 4, buf ^ 1);
+      const int kd_next = doc_of(t + 4);
+      compute(t, buf, kd);
+      // this tile's LDS reads end before the next copy may overwrite it
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      kd = kd_next;
+    }
+  } else {
+    // tiles in turn; where documents are used, those that hold none of the
+    // block's are passed over (32 tiles are looked through at a time)
+    int group = -1;
+    uint32_t bits = 0;
+    auto next = [&](int t) -> int {
+      if (!use_docs) return t;
+      while (t < t_end) {
+        if (t >> 5 != group) {
+          group = t >> 5;
+          bits = 0;
+#pragma unroll 8
+          for (int k = 0; k < 32; ++k) {
+            const int j = (32 * group + k) * TK + lane;
+            const int kd = j < n ? a.k_doc[(size_t)b * a.Skv + j] : 0;
+            bits |= (__any(j < n && kd >= doc_lo && kd <= doc_hi) ? 1u : 0u) << k;
+          }
+        }
+        const uint32_t left = bits >> (t & 31);
+        if (left) return min(t_end, t + __builtin_ctz(left));
+        t = (t | 31) + 1;
+      }
+      return t_end;
+    };
+    int t = next(t_begin);
+    if (t < t_end) copy_tile(t, 0);
+    int kd = doc_of(t);
+    auto step = [&](int buf) __attribute__((always_inline)) {
+      dma_wait();
+      __syncthreads();
+      const int tn = next(t + 1);
+      if (tn < t_end) copy_tile(tn, buf ^ 1);
+      const int kd_next = doc_of(tn);
+      if (t * TK < lim_last) compute(t, buf, kd);
+      kd = kd_next;
+      t = tn;
+    };
+    while (t < t_end) {
+      step(0);
+      if (t >= t_end) break;
+      step(1);
+    }
+  }
+
+  l = half_sum(l);
+
+  if constexpr (KEYS) {
+    // join the waves: O^T, m and l of waves 1..3 through LDS (their buffers
+    // are no longer needed), wave 0 goes on alone
+    __syncthreads();
+    float* jo = reinterpret_cast<float*>(lds);                 // [4][32 rows][DP + 4]
+    float* jm = reinterpret_cast<float*>(lds) + 4 * 32 * (DP + 4);
+    if (half == 0) {
+      jm[(wave * 32 + l32) * 2] = m;
+      jm[(wave * 32 + l32) * 2 + 1] = l;
+    }
+    if (wave > 0) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<b4f*>(jo + (wave * 32 + l32) * (DP + 4) + 32 * d + 8 * g + 4 * half) =
+              (b4f){o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    float up = m;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) up = fmaxf(up, jm[(w * 32 + l32) * 2]);
+    const float f0 = exp2_(m - up);
+    l *= f0;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= f0;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      const float f = exp2_(jm[(w * 32 + l32) * 2] - up);
+      l = fmaf(f, jm[(w * 32 + l32) * 2 + 1], l);
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const b4f x = *reinterpret_cast<const b4f*>(jo + (w * 32 + l32) * (DP + 4) + 32 * d + 8 * g + 4 * half);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[d][4 * g + i] = fmaf(f, x[i], o[d][4 * g + i]);
+        }
+    }
+    m = up;
+  }
+
+  // ---- rows that are not finite are computed again, the others stored
+  bool bad = !(fabsf(l) < __builtin_inff());
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bad = bad || !(fabsf(o[d][i]) < __builtin_inff());
+  const bool real = row0 + l32 < p.R;
+  const uint64_t who = __ballot(bad && real);
+  const uint32_t again = (uint32_t)(who | (who >> 32));
+  const size_t rows_all = (size_t)p.groups * p.R;
+  const bool parts = p.part.splits > 1;
+  if (real && !((again >> l32) & 1)) {
+    if (parts) {
+      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + row;
+      float* op = p.part.o + at * DP;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<b4f*>(op + 32 * d + 8 * g + 4 * half) =
+              (b4f){o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+      if (half == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(m, l);
+    } else {
+      const float by = l != 0.f ? 1.0f / l : 0.f;
+      uint16_t* op = a.o + b * a.o_batch + qi * a.o_token + qh * a.o_head;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int at = 32 * d + 8 * g + 4 * half;
+          if (!PAD || at < a.D)
+            *reinterpret_cast<uint2*>(op + at) = make_uint2(narrow2<DT>(o[d][4 * g] * by, o[d][4 * g + 1] * by),
+                                                            narrow2<DT>(o[d][4 * g + 2] * by, o[d][4 * g + 3] * by));
+        }
+    }
+  }
+  for (uint32_t left = again; left; left &= left - 1) {
+    const int r = row0 + __builtin_ctz(left);
+    float rm, rl;
+    b2f ro;
+    row_again<DT>(p, b, hk, r, n, t_begin * TK, min(n, t_end * TK), &rm, &rl, &ro);
+    if (parts) {
+      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + r;
+      if (2 * lane < DP) *reinterpret_cast<b2f*>(p.part.o + at * DP + 2 * lane) = ro;
+      if (lane == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(rm, rl);
+    } else if (2 * lane < a.D) {
+      const float by = rl != 0.f ? 1.0f / rl : 0.f;
+      uint16_t* op = a.o + b * a.o_batch + (r / p.G) * a.o_token + (hk * p.G + r % p.G) * a.o_head;
+      *reinterpret_cast<uint32_t*>(op + 2 * lane) = narrow2<DT>(ro[0] * by, ro[1] * by);
+    }
+  }
+}
+
+// Joins the parts of a row: a quarter wave (16 lanes) per row, 8 elements a lane.
+template <int DT, int DP>
+__global__ __launch_bounds__(256) void join_kernel(AttnP p) {
+  const svdq_attention_args& a = p.a;
+  constexpr int LPR = DP / 8;
+  const size_t rows = (size_t)p.groups * p.R;
+  const size_t at = (size_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  const int d = 8 * (threadIdx.x % LPR);
+  if (at >= rows || d >= a.D) return;
+  float top = kLow;
+  for (int s = 0; s < p.part.splits; ++s) top = fmaxf(top, p.part.ml[2 * (s * rows + at)]);
+  float sum = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int s = 0; s < p.part.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part.ml + 2 * (s * rows + at));
+    const float f = exp2_(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+    const float* op = p.part.o + (s * rows + at) * DP + d;
+    const b4f x = *reinterpret_cast<const b4f*>(op), y = *reinterpret_cast<const b4f*>(op + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[i] = fmaf(f, x[i], o[i]);
+      o[4 + i] = fmaf(f, y[i], o[4 + i]);
+    }
+  }
   const float by = sum != 0.f ? 1.0f / sum : 0.f;
-  if (live)
-    *reinterpret_cast<uint32_t*>(a.o + b * a.o_batch + i * a.o_token + h * a.o_head + 2 * lane) =
-        narrow2<DT>(o[0] * by, o[1] * by);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] *= by;
+  const int grp = (int)(at / p.R), r = (int)(at % p.R);
+  uint16_t* op = a.o + (grp / a.Hkv) * a.o_batch + (r / p.G) * a.o_token +
+                 ((grp % a.Hkv) * p.G + r % p.G) * a.o_head + d;
+  *reinterpret_cast<b4i*>(op) = narrow8<DT>(o);
 }
 
 svdq_status check(const svdq_attention_args* a) {
@@ -58,7 +571,7 @@ svdq_status check(const svdq_attention_args* a) {
   if (a->B < 1 || a->Sq < 1 || a->Sq > lim || a->Skv < 0 || a->Skv > lim || a->Hq < 1 || a->Hkv < 1 ||
       a->Hq > 65536 || a->Hq % a->Hkv != 0 || a->D < 8 || a->D > SVDQ_ATTENTION_MAX_HEAD_DIM || a->D % 8 != 0)
     return SVDQ_ERR_SHAPE;
-  if ((int64_t)a->B * a->Hq > (1 << 24) || (int64_t)a->B * a->Hq * a->Sq > (int64_t)1 << 31) return SVDQ_ERR_SHAPE;
+  if ((int64_t)a->B * a->Hq > (1 << 24) || (int64_t)a->B * a->Hq * a->Sq > (int64_t)1 << 30) return SVDQ_ERR_SHAPE;
   if (a->Skv > 0 && (!a->k || !a->v)) return SVDQ_ERR_ARG;
   if ((a->q_doc == nullptr) != (a->k_doc == nullptr) && a->Skv > 0) return SVDQ_ERR_ARG;
   const float big = 3.0e38f;
@@ -67,10 +580,59 @@ svdq_status check(const svdq_attention_args* a) {
                         a->v_batch, a->v_token, a->v_head, a->o_batch, a->o_token, a->o_head};
   for (int64_t s : st)
     if (s % 8 != 0) return SVDQ_ERR_ALIGN;
+  if (a->k_token < 0 || a->v_token < 0 || a->k_token > (1 << 28) || a->v_token > (1 << 28)) return SVDQ_ERR_SHAPE;
   if (!on16(a->q) || !on16(a->k) || !on16(a->v) || !on16(a->o) || !on4(a->slopes) || !on4(a->kv_len) ||
       !on4(a->prefix) || !on4(a->q_doc) || !on4(a->k_doc))
     return SVDQ_ERR_ALIGN;
   return SVDQ_OK;
+}
+
+// The arrangement of a call: by its sizes alone, so that a workspace fits
+// every call of its shape.
+struct Plan {
+  bool keys;
+  int G, R, tiles, groups, splits;
+  size_t rows() const { return (size_t)groups * R; }
+};
+Plan plan_of(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_t D) {
+  Plan p;
+  p.G = Hq / Hkv;
+  p.R = Sq * p.G;
+  p.groups = B * Hkv;
+  p.keys = p.R <= 32;
+  p.tiles = p.keys ? 1 : (p.R + 127) / 128;
+  const int64_t blocks = (int64_t)p.tiles * p.groups;
+  const int64_t want = p.keys ? 4 * kCus : 2 * kCus;        // blocks that fill the chip
+  const int64_t least = p.keys ? 512 : 512;                 // keys worth a block of their own
+  const int64_t most = ((int64_t)Skv + least - 1) / least;
+  int64_t s = (want + blocks - 1) / blocks;
+  if (s > most) s = most;
+  if (s > 64) s = 64;
+  p.splits = s < 1 ? 1 : (int)s;
+  (void)D;
+  return p;
+}
+int padded_dim(int32_t D) { return D <= 64 ? 64 : 128; }
+
+template <int DT, int DP, bool PAD>
+svdq_status launch3(const AttnP& p, const Plan& pl, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)pl.tiles * pl.groups * pl.splits));
+  if (pl.keys) hipLaunchKernelGGL((attention_kernel<DT, DP, PAD, true>), grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((attention_kernel<DT, DP, PAD, false>), grid, dim3(256), 0, st, p);
+  svdq_status s = launched();
+  if (s == SVDQ_OK && pl.splits > 1) {
+    const int per = 256 / (DP / 8);
+    hipLaunchKernelGGL((join_kernel<DT, DP>), dim3((unsigned)((pl.rows() + per - 1) / per)), dim3(256), 0, st, p);
+    s = launched();
+  }
+  return s;
+}
+template <int DT>
+svdq_status launch2(const AttnP& p, const Plan& pl, hipStream_t st) {
+  if (p.a.D == 128) return launch3<DT, 128, false>(p, pl, st);
+  if (p.a.D > 64) return launch3<DT, 128, true>(p, pl, st);
+  if (p.a.D == 64) return launch3<DT, 64, false>(p, pl, st);
+  return launch3<DT, 64, true>(p, pl, st);
 }
 
 }  // namespace
@@ -80,8 +642,12 @@ using namespace svdq;
 
 extern "C" size_t svdq_attention_workspace_bytes(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv,
                                                  int32_t D) {
-  (void)B, (void)Sq, (void)Skv, (void)Hq, (void)Hkv, (void)D;
-  return 0;
+  if (B < 1 || Sq < 1 || Skv < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 8 || D > SVDQ_ATTENTION_MAX_HEAD_DIM ||
+      (int64_t)B * Hq > (1 << 24) || (int64_t)B * Hq * Sq > (int64_t)1 << 30)
+    return 0;
+  const Plan p = plan_of(B, Sq, Skv, Hq, Hkv, D);
+  if (p.splits == 1) return 0;
+  return align256(p.splits * p.rows() * padded_dim(D) * 4) + align256(p.splits * p.rows() * 8);
 }
 
 extern "C" svdq_status svdq_attention(const svdq_attention_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -91,10 +657,28 @@ extern "C" svdq_status svdq_attention(const svdq_attention_args* a, void* ws, si
   if (need > 0 && (!ws || ws_bytes < need)) return !ws ? SVDQ_ERR_ARG : SVDQ_ERR_WORKSPACE;
   if (((uintptr_t)ws & 255u) != 0) return SVDQ_ERR_ALIGN;
   if ((s = device_ok()) != SVDQ_OK) return s;
+  const Plan pl = plan_of(a->B, a->Sq, a->Skv, a->Hq, a->Hkv, a->D);
+  AttnP p;
+  p.a = *a;
+  p.G = pl.G;
+  p.R = pl.R;
+  p.tiles = pl.tiles;
+  p.groups = pl.groups;
+  // A negative scale turns the signs of Q, scale 0 makes Q zero; what remains
+  // is positive, so a hidden score of -infinity stays one when scaled.
+  constexpr float log2e = 1.44269504088896f;
+  const float scale = a->scale < 0.f ? -a->scale : a->scale > 0.f ? a->scale : 1.f;
+  p.flip = a->scale < 0.f;
+  p.qmul = a->scale < 0.f ? -1.f : a->scale > 0.f ? 1.f : 0.f;
+  p.c1 = scale * log2e;
+  p.c2 = a->softcap > 0.f ? 2.f * scale / a->softcap * log2e : 0.f;
+  p.c3 = a->softcap * log2e;
+  p.part.splits = pl.splits;
+  p.part.o = static_cast<float*>(ws);
+  p.part.ml = pl.splits > 1
+                  ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                             align256(pl.splits * pl.rows() * padded_dim(a->D) * 4))
+                  : nullptr;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int64_t rows = (int64_t)a->B * a->Hq * a->Sq;
-  const dim3 grid((unsigned)((rows + 3) / 4)), block(256);
-  if (a->dtype == SVDQ_BF16) hipLaunchKernelGGL((attention_row_kernel<SVDQ_BF16>), grid, block, 0, st, *a);
-  else hipLaunchKernelGGL((attention_row_kernel<SVDQ_FP16>), grid, block, 0, st, *a);
-  return launched();
+  return a->dtype == SVDQ_BF16 ? launch2<SVDQ_BF16>(p, pl, st) : launch2<SVDQ_FP16>(p, pl, st);
 }

@@ -57,6 +57,35 @@ __device__ __forceinline__ b4i narrow8(const float* f) {
   return v;
 }
 
+#define SVDQ_LDS __attribute__((address_space(3)))
+
+// One wave-wide 1 KB direct-to-LDS copy: lane i's 16 bytes at base + off
+// (base wave-uniform, off per lane) land at LDS byte lds + 16 i; inactive
+// lanes copy nothing.  Issued from asm so that the compiler does not serialise
+// it against unrelated LDS reads: completion is waited for explicitly
+// (dma_wait).  M0 is restored before the asm block ends.
+__device__ __forceinline__ void dma_16(const uint8_t* base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "global_load_lds_dwordx4 %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
+      : "memory");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(size_t)(SVDQ_LDS const uint8_t*)p; }
+
+// Blocks are dealt to the 8 XCDs round robin.  xcd_order() maps the block
+// index so that each XCD gets one contiguous run of work ids, whose operands
+// then share its L2.
+__device__ __forceinline__ int xcd_order(int b, int total) {
+  const int q = total >> 3, r = total & 7, x = b & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+
 inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool on4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 inline bool is_dtype(int32_t d) { return d == SVDQ_BF16 || d == SVDQ_FP16; }
