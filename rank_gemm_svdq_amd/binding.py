@@ -9,6 +9,7 @@ no fallback.
 
 import ctypes as C
 import os
+import struct
 
 import numpy as np
 
@@ -170,10 +171,10 @@ def lib():
                                             vp, vp, vp]
     L.svdq_fp8_linear.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
     L.svdq_rope_frequencies.argtypes = [i32, vp, C.c_double, i32, vp, vp]
-    L.svdq_rope.argtypes = [C.POINTER(RopeArgs), vp]
+    L.svdq_rope.argtypes = [vp, vp]             # svdq_rope_args
     L.svdq_attention_workspace_bytes.restype = sz
     L.svdq_attention_workspace_bytes.argtypes = [i32] * 6
-    L.svdq_attention.argtypes = [C.POINTER(AttentionArgs), vp, sz, vp]
+    L.svdq_attention.argtypes = [vp, vp, sz, vp]   # svdq_attention_args
     for name in ("svdq_device_check", "svdq_layer_sizes", "svdq_workspace_layout", "svdq_calib_absmax",
                  "svdq_pack_host", "svdq_prepare", "svdq_attach_lora", "svdq_kernel_layout",
                  "svdq_unpack_activations", "svdq_quantize_lora_down", "svdq_gemm_lora_up",
@@ -534,62 +535,91 @@ def reservoir_select(n_calls, k, seed):
 
 
 # ------------------------------------------- the operators around the layer
+#
+# Short calls are bound by what happens before the launch, so the checks here
+# are one expression per tensor (the message is put together only on a
+# refusal) and argument structures are packed in one go.
 
 FP8_BLOCK = 128                 # SVDQ_FP8_BLOCK
 ROPE_MAX_AXES = 8               # SVDQ_ROPE_MAX_AXES
 ATTENTION_MAX_HEAD_DIM = 128    # SVDQ_ATTENTION_MAX_HEAD_DIM
-_VALUE_TYPES = None             # torch dtype -> svdq_dtype, made on first use
+_ROPE_PACK = struct.Struct("6i3Q2Q2Q2i8q")
+_ATTENTION_PACK = struct.Struct("8i2f4Q12q5Q")
+assert _ROPE_PACK.size == C.sizeof(RopeArgs) and _ATTENTION_PACK.size == C.sizeof(AttentionArgs)
 
 
-def _value_type(t, what, where):
-    """svdq_dtype of a tensor; bf16 bit patterns may come as int16, as in the rest of the binding."""
-    global _VALUE_TYPES
-    if _VALUE_TYPES is None:
-        torch = _torch()
-        _VALUE_TYPES = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 1}
-    code = _VALUE_TYPES.get(t.dtype)
-    if code is None:
-        raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected bfloat16, float16 or int16 (bf16 bits)")
-    return code
+class _Torch:
+    """What the operators need of torch, looked up on first use."""
+
+    def __init__(self):
+        import torch
+        self.f32, self.i32 = torch.float32, torch.int32
+        self.values = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 1}   # -> svdq_dtype (int16: bf16 bits)
+        self.codes = (torch.float8_e4m3fn, torch.uint8)
+        self.bytes = torch.uint8
+        self.current_device = torch.cuda.current_device
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _want(t, what, where, dev, shape=None, dtypes=None, contiguous=True):
-    """A GPU tensor on `dev` of this shape (None: any extent) and type."""
-    if t.device != dev:
-        raise SvdqError(1, f"{where}: {what} is on {t.device}, expected {dev}")
+_T = None
+
+
+def _tt():
+    global _T
+    if _T is None:
+        _T = _Torch()
+    return _T
+
+
+def _refuse(t, what, where, dev, shape, dtypes, contiguous):
+    """Say what is wrong with a tensor."""
+    if t.get_device() != dev:
+        raise SvdqError(1, f"{where}: {what} is on {t.device}, expected cuda:{dev}")
     if dtypes is not None and t.dtype not in dtypes:
         raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if shape is not None and t.shape != shape:
         raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise SvdqError(1, f"{where}: {what} is not contiguous")
-    elif t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise SvdqError(1, f"{where}: the last dimension of {what} is not contiguous")
+    raise SvdqError(1, f"{where}: {what} is not contiguous" if contiguous
+                    else f"{where}: the last dimension of {what} is not contiguous")
+
+
+def _whole(t, dev, shape, dtype, what, where):
+    """Address of a contiguous tensor of this device, shape and type."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, what, where, dev, shape, (dtype,), True)
     return t.data_ptr()
 
 
-def _on_gpu(t, what, where):
-    if not t.is_cuda:
+def _codes(t, dev, what, where):
+    """Address of a contiguous tensor of E4M3 codes."""
+    if t.dtype not in _T.codes or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, what, where, dev, None, _T.codes, True)
+    return t.data_ptr()
+
+
+def _rows(t, dev, shape, dtype, what, where):
+    """Address and strides of a tensor whose last dimension is contiguous."""
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (st[-1] != 1 and shape[-1] > 1):
+        _refuse(t, what, where, dev, shape, (dtype,), False)
+    return t.data_ptr(), st
+
+
+def _first(t, dims, what, where):
+    """(device index, svdq_dtype) of the tensor that the others of a call go by."""
+    T = _tt()
+    dev = t.get_device()
+    if dev < 0:
         raise SvdqError(1, f"{where}: {what} is not in GPU memory")
-    torch = _torch()
-    if t.device.index != torch.cuda.current_device():
-        raise SvdqError(1, f"{where}: {what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
-
-
-def _stream_on(stream, dev):
-    return (_torch().cuda.current_stream(dev) if stream is None else stream).cuda_stream
-
-
-def _strides(t, extents):
-    """Strides in elements; those of dimensions with one place, which address nothing, as 0."""
-    return [s if n > 1 else 0 for s, n in zip(t.stride(), extents)]
-
-
-def _fp8_types():
-    torch = _torch()
-    return (torch.float8_e4m3fn, torch.uint8)
+    if dev != T.current_device():
+        raise SvdqError(1, f"{where}: {what} is on {t.device}, the current device is cuda:{T.current_device()}")
+    code = T.values.get(t.dtype)
+    if code is None:
+        raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected bfloat16, float16 or int16 (bf16 bits)")
+    if t.dim() != dims:
+        raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {dims} dimensions")
+    return dev, code
 
 
 def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=None):
@@ -599,25 +629,25 @@ def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=Non
     q [M, K] float8_e4m3fn or uint8; s [M, ceil(K / 128)] float32.  Writes q, s
     and, if given, h."""
     where = "svdq_add_rmsnorm_quantize"
-    torch = _torch()
-    dev = _on_gpu(x, "x", where)
-    dt = _value_type(x, "x", where)
-    if x.dim() != 2:
-        raise SvdqError(2, f"{where}: x has shape {tuple(x.shape)}, expected (M, K)")
-    M, K = x.shape
-    own = (x.dtype,)
-    xp = _want(x, "x", where, dev, contiguous=False)
-    wp = _want(weight, "weight", where, dev, (K,), own)
-    qp = _want(q, "q", where, dev, (M, K), _fp8_types())
-    sp = _want(s, "s", where, dev, (M, -(-K // FP8_BLOCK)), (torch.float32,))
-    row = lambda t: t.stride(0) if M > 1 else K
-    rp, rs, hp, hs = None, 0, None, 0
+    dev, dt = _first(x, 2, "x", where)
+    shape, own = x.shape, x.dtype
+    M, K = shape
+    xp, xs = _rows(x, dev, shape, own, "x", where)
+    rp, rs, hp, hs = None, (0,), None, (0,)
     if residual is not None:
-        rp, rs = _want(residual, "residual", where, dev, (M, K), own, contiguous=False), row(residual)
+        rp, rs = _rows(residual, dev, shape, own, "residual", where)
     if h is not None:
-        hp, hs = _want(h, "h", where, dev, (M, K), own, contiguous=False), row(h)
-    _check(lib().svdq_add_rmsnorm_quantize(xp, row(x), rp, rs, wp, eps, M, K, dt, hp, hs, qp, sp,
-                                           _stream_on(stream, dev)), where)
+        hp, hs = _rows(h, dev, shape, own, "h", where)
+    if q.shape != shape:
+        _refuse(q, "q", where, dev, shape, _T.codes, True)
+    # the stride of a single row addresses nothing and may be anything
+    st = lib().svdq_add_rmsnorm_quantize(
+        xp, xs[0] if M > 1 else K, rp, rs[0] if M > 1 else K, _whole(weight, dev, (K,), own, "weight", where), eps, M, K,
+        dt, hp, hs[0] if M > 1 else K, _codes(q, dev, "q", where),
+        _whole(s, dev, (M, -(-K // FP8_BLOCK)), _T.f32, "s", where),
+        _T.stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvdqError(st, where)
 
 
 def fp8_linear(xq, xs, wq, ws, Y, bias=None, stream=None):
@@ -625,20 +655,21 @@ def fp8_linear(xq, xs, wq, ws, Y, bias=None, stream=None):
     wq [N, K] (float8_e4m3fn or uint8) and fp32 scales xs [M, K / 128],
     ws [ceil(N / 128), K / 128]; bias [N] has Y's type.  Writes Y [M, N]."""
     where = "svdq_fp8_linear"
-    f32 = (_torch().float32,)
-    dev = _on_gpu(xq, "xq", where)
-    if xq.dim() != 2 or wq.dim() != 2 or wq.shape[1] != xq.shape[1]:
-        raise SvdqError(2, f"{where}: xq {tuple(xq.shape)} and wq {tuple(wq.shape)}, expected (M, K) and (N, K)")
-    M, K = xq.shape
-    N = wq.shape[0]
-    dt = _value_type(Y, "Y", where)
-    codes = _fp8_types()
-    xp, wp = _want(xq, "xq", where, dev, None, codes), _want(wq, "wq", where, dev, None, codes)
-    sp = _want(xs, "xs", where, dev, (M, K // FP8_BLOCK), f32)
-    tp = _want(ws, "ws", where, dev, (-(-N // FP8_BLOCK), K // FP8_BLOCK), f32)
-    yp = _want(Y, "Y", where, dev, (M, N))
-    bp = None if bias is None else _want(bias, "bias", where, dev, (N,), (Y.dtype,))
-    _check(lib().svdq_fp8_linear(xp, sp, wp, tp, bp, M, K, N, dt, yp, _stream_on(stream, dev)), where)
+    dev, dt = _first(Y, 2, "Y", where)
+    M, N = Y.shape
+    if xq.dim() != 2 or xq.shape[0] != M or wq.shape != (N, xq.shape[1]):
+        raise SvdqError(2, f"{where}: xq {tuple(xq.shape)}, wq {tuple(wq.shape)} and Y ({M}, {N}), expected (M, K), "
+                           "(N, K) and (M, N)")
+    K = xq.shape[1]
+    kb = K // FP8_BLOCK
+    f32 = _T.f32
+    st = lib().svdq_fp8_linear(
+        _codes(xq, dev, "xq", where), _whole(xs, dev, (M, kb), f32, "xs", where), _codes(wq, dev, "wq", where),
+        _whole(ws, dev, (-(-N // FP8_BLOCK), kb), f32, "ws", where),
+        None if bias is None else _whole(bias, dev, (N,), Y.dtype, "bias", where), M, K, N, dt,
+        _whole(Y, dev, (M, N), Y.dtype, "Y", where), _T.stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvdqError(st, where)
 
 
 def rope_frequencies(dims, theta=10000.0, shared=False):
@@ -673,33 +704,34 @@ def rope(plan, positions, x, y, x2=None, y2=None, stream=None):
     [M, heads, head_dim], x2, y2 [M, heads2, head_dim], any token and head
     strides that are multiples of 8 elements; y may be x."""
     where = "svdq_rope"
-    dev = _on_gpu(x, "x", where)
-    dt = _value_type(x, "x", where)
-    if x.dim() != 3:
-        raise SvdqError(2, f"{where}: x has shape {tuple(x.shape)}, expected (M, heads, head_dim)")
-    M, H, D = x.shape
-    own = (x.dtype,)
-    i32 = (_torch().int32,)
-    a = RopeArgs(M, plan.axes, plan.pairs, D, int(plan.interleaved), dt,
-                 _want(positions, "positions", where, dev, (M, plan.axes), i32),
-                 _want(plan.turns, "the plan's turns", where, dev), _want(plan.axis, "the plan's axis", where, dev))
-    a.x[0] = _want(x, "x", where, dev, contiguous=False)
-    a.y[0] = _want(y, "y", where, dev, x.shape, own, contiguous=False)
-    a.heads[0] = H
-    a.x_token[0], a.x_head[0] = _strides(x, (M, H))
-    a.y_token[0], a.y_head[0] = _strides(y, (M, H))
-    if (x2 is None) != (y2 is None):
+    dev, dt = _first(x, 3, "x", where)
+    shape, own = x.shape, x.dtype
+    M, H, D = shape
+    xp, xs = _rows(x, dev, shape, own, "x", where)
+    yp, ys = _rows(y, dev, shape, own, "y", where)
+    x2p = y2p = H2 = 0
+    x2s = y2s = (0, 0)
+    if x2 is not None and y2 is not None:
+        shape2 = x2.shape
+        if len(shape2) != 3 or shape2[0] != M or shape2[2] != D:
+            raise SvdqError(2, f"{where}: x2 has shape {tuple(shape2)}, expected ({M}, heads, {D})")
+        H2 = shape2[1]
+        x2p, x2s = _rows(x2, dev, shape2, own, "x2", where)
+        y2p, y2s = _rows(y2, dev, shape2, own, "y2", where)
+    elif x2 is not None or y2 is not None:
         raise SvdqError(1, f"{where}: x2 and y2 go together")
-    if x2 is not None:
-        if x2.dim() != 3 or x2.shape[0] != M or x2.shape[2] != D:
-            raise SvdqError(2, f"{where}: x2 has shape {tuple(x2.shape)}, expected ({M}, heads, {D})")
-        H2 = x2.shape[1]
-        a.x[1] = _want(x2, "x2", where, dev, None, own, contiguous=False)
-        a.y[1] = _want(y2, "y2", where, dev, x2.shape, own, contiguous=False)
-        a.heads[1] = H2
-        a.x_token[1], a.x_head[1] = _strides(x2, (M, H2))
-        a.y_token[1], a.y_head[1] = _strides(y2, (M, H2))
-    _check(lib().svdq_rope(C.byref(a), _stream_on(stream, dev)), where)
+    # strides of dimensions with one place address nothing: 0
+    t = M > 1
+    h, h2 = H > 1, H2 > 1
+    a = _ROPE_PACK.pack(M, plan.axes, plan.pairs, D, plan.interleaved, dt,
+                        _whole(positions, dev, (M, plan.axes), _T.i32, "positions", where),
+                        _whole(plan.turns, dev, (plan.pairs, 2), _T.f32, "the plan's turns", where),
+                        _whole(plan.axis, dev, (plan.pairs,), _T.i32, "the plan's axis", where),
+                        xp, x2p, yp, y2p, H, H2, xs[0] * t, x2s[0] * t, xs[1] * h, x2s[1] * h2,
+                        ys[0] * t, y2s[0] * t, ys[1] * h, y2s[1] * h2)
+    st = lib().svdq_rope(a, _T.stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvdqError(st, where)
 
 
 def attention_workspace_bytes(B, Sq, Skv, Hq, Hkv, D):
@@ -721,34 +753,35 @@ def attention(q, k, v, o, ws, scale=None, causal=False, softcap=0.0, slopes=None
     if None.  slopes [Hq] float32; kv_len, prefix [B], q_doc [B, Sq], k_doc
     [B, Skv] int32.  The queries are the last Sq of the kv_len keys' positions."""
     where = "svdq_attention"
-    torch = _torch()
-    dev = _on_gpu(q, "q", where)
-    dt = _value_type(q, "q", where)
-    if q.dim() != 4 or k.dim() != 4 or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
-        raise SvdqError(2, f"{where}: q {tuple(q.shape)} and k {tuple(k.shape)}, expected (B, Sq, Hq, D) and "
+    dev, dt = _first(q, 4, "q", where)
+    shape, kshape, own = q.shape, k.shape, q.dtype
+    B, Sq, Hq, D = shape
+    if len(kshape) != 4 or kshape[0] != B or kshape[3] != D:
+        raise SvdqError(2, f"{where}: q {tuple(shape)} and k {tuple(kshape)}, expected (B, Sq, Hq, D) and "
                            "(B, Skv, Hkv, D)")
-    B, Sq, Hq, D = q.shape
-    Skv, Hkv = k.shape[1], k.shape[2]
-    own, i32 = (q.dtype,), (torch.int32,)
-    a = AttentionArgs(B, Sq, Skv, Hq, Hkv, D, dt, int(bool(causal)), D ** -0.5 if scale is None else scale, softcap,
-                      _want(q, "q", where, dev, contiguous=False),
-                      _want(k, "k", where, dev, None, own, contiguous=False),
-                      _want(v, "v", where, dev, k.shape, own, contiguous=False),
-                      _want(o, "o", where, dev, q.shape, own, contiguous=False),
-                      *_strides(q, (B, Sq, Hq)), *_strides(k, (B, Skv, Hkv)), *_strides(v, (B, Skv, Hkv)),
-                      *_strides(o, (B, Sq, Hq)))
-    if slopes is not None:
-        a.slopes = _want(slopes, "slopes", where, dev, (Hq,), (torch.float32,))
-    if kv_len is not None:
-        a.kv_len = _want(kv_len, "kv_len", where, dev, (B,), i32)
-    if prefix is not None:
-        a.prefix = _want(prefix, "prefix", where, dev, (B,), i32)
+    Skv, Hkv = kshape[1], kshape[2]
+    qp, qs = _rows(q, dev, shape, own, "q", where)
+    kp, ks = _rows(k, dev, kshape, own, "k", where)
+    vp, vs = _rows(v, dev, kshape, own, "v", where)
+    op, os_ = _rows(o, dev, shape, own, "o", where)
+    i32 = _T.i32
     if (q_doc is None) != (k_doc is None):
         raise SvdqError(1, f"{where}: q_doc and k_doc go together")
-    if q_doc is not None:
-        a.q_doc = _want(q_doc, "q_doc", where, dev, (B, Sq), i32)
-        a.k_doc = _want(k_doc, "k_doc", where, dev, (B, Skv), i32)
+    # strides of dimensions with one place address nothing: 0
+    b, i, h, j, g = B > 1, Sq > 1, Hq > 1, Skv > 1, Hkv > 1
+    a = _ATTENTION_PACK.pack(
+        B, Sq, Skv, Hq, Hkv, D, dt, bool(causal), D ** -0.5 if scale is None else scale, softcap, qp, kp, vp, op,
+        qs[0] * b, qs[1] * i, qs[2] * h, ks[0] * b, ks[1] * j, ks[2] * g, vs[0] * b, vs[1] * j, vs[2] * g,
+        os_[0] * b, os_[1] * i, os_[2] * h,
+        0 if slopes is None else _whole(slopes, dev, (Hq,), _T.f32, "slopes", where),
+        0 if kv_len is None else _whole(kv_len, dev, (B,), i32, "kv_len", where),
+        0 if prefix is None else _whole(prefix, dev, (B,), i32, "prefix", where),
+        0 if q_doc is None else _whole(q_doc, dev, (B, Sq), i32, "q_doc", where),
+        0 if k_doc is None else _whole(k_doc, dev, (B, Skv), i32, "k_doc", where))
     wp, wn = None, 0
     if ws is not None:
-        wp, wn = _want(ws, "workspace", where, dev, None, (torch.uint8,)), ws.numel()
-    _check(lib().svdq_attention(C.byref(a), wp if wn else None, wn, _stream_on(stream, dev)), where)
+        wn = ws.numel()
+        wp = _whole(ws, dev, ws.shape, _T.bytes, "workspace", where) if wn else None
+    st = lib().svdq_attention(a, wp, wn, _T.stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvdqError(st, where)

@@ -75,6 +75,18 @@ __device__ __forceinline__ void dma_16(const uint8_t* base, uint32_t off, uint32
       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
       : "memory");
 }
+// The same with 4 bytes a lane (256 bytes).
+__device__ __forceinline__ void dma_4(const uint8_t* base, uint32_t off, uint32_t lds) {
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "global_load_lds_dword %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
+      : "memory");
+}
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(size_t)(SVDQ_LDS const uint8_t*)p; }
 
