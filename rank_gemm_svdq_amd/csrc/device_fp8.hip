@@ -45,32 +45,48 @@ __device__ __forceinline__ void add_bias8(const uint16_t* bias, int n, float* v)
   for (int i = 0; i < 8; ++i) v[i] += t[i];
 }
 
-// ---------------------------------------------------------- large tiles
+// ------------------------------------------------------------ LDS tiles
 //
-// A block computes BM tokens x BN out-features; its waves (WM x WN) own MT x
-// NT MFMA tiles each.  Steps of 128 k of both operands go to LDS by direct
-// copies (1 KB: 8 rows x 128 codes), one step ahead, two buffers, one barrier
-// a step.  Chunk c of a row sits at slot c ^ f(row) with f such that the 16
-// lanes served together in a fragment read hit distinct 16-byte slots.
+// A block computes BM tokens x BN out-features; WM x WN waves own MT x NT MFMA
+// tiles each, and WK such groups of waves take the steps of 128 k in turn
+// (joined in LDS at the end).  Codes and token scales of the next step go to
+// LDS by direct copies (1 KB: 8 rows x 128 codes), two buffers, one barrier a
+// step.
+// Chunk c of a row sits at slot c ^ f(row) with f such that the 16 lanes
+// served together in a fragment read hit distinct 16-byte slots.
+//
+// The block sums of a pair of weight tiles are scaled while the MFMAs of the
+// next pair run (two sets of them), and the token codes of the next tile are
+// read ahead.  Two waves a SIMD hide most of the widening and scaling behind
+// the other's MFMAs.  4096 x 3072 -> 9216 in 128 x 128 tiles, two blocks a
+// compute unit: 214 us, 1.08 PFLOP/s (a large bf16 product of the vendor's
+// library: 1.21); without the copies it would take 180 us, without the
+// widening 203 us.
 
-template <int NT, int MT, int WN, int WM>
-struct LargeTile {
+template <int NT, int MT, int WN, int WM, int WK>
+struct Tile {
   static constexpr int WAVES = WN * WM, BN = 16 * NT * WN, BM = 16 * MT * WM;
-  static constexpr int STEP = (BN + BM) * 128;
+  static constexpr int CODES = (BN + BM) * 128;             // of a step
+  static constexpr int STEP = CODES + WAVES * 256;          // and 64 token scales per wave
+  static constexpr int UNITS = (BN + BM) / 8 / WAVES;       // code copies per wave and step
+  static constexpr int JOIN = WK > 1 ? (WK - 1) * BN * BM * 4 : 0;
+  static constexpr int LDS = 2 * WK * STEP > JOIN ? 2 * WK * STEP : JOIN;
 };
 
-template <int DT, int NT, int MT, int WN, int WM>
-__global__ __launch_bounds__(64 * WN * WM, 2) void fp8_large_kernel(
+template <int DT, int NT, int MT, int WN, int WM, int WK>
+__global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, int M, int K, int N, uint16_t* __restrict__ Y,
     int tiles_m, int tiles_n) {
-  using T = LargeTile<NT, MT, WN, WM>;
-  constexpr int UNITS = (T::BN + T::BM) / 8 / T::WAVES;   // copies per wave and step
-  static_assert((T::BN / 8) % UNITS == 0, "a wave copies rows of one operand");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * T::STEP];
-  __shared__ float sxl[2][T::BM];
+  using T = Tile<NT, MT, WN, WM, WK>;
+  constexpr int UNITS = T::UNITS;
+  static_assert(MT <= 4 && NT % 2 == 0, "64 token scales per wave, pairs of weight tiles");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_all[T::LDS];
+  __shared__ float swl[512];                               // K <= 65536
+  static_assert(128 % T::BN == 0, "one block of weight scales");
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wk = wave_all / T::WAVES, wave = wave_all % T::WAVES;
   const int wm = wave % WM, wn = wave / WM;
   const int l16 = lane & 15, g = lane >> 4;
   // work ids run through groups of 8 token tiles, out-feature tile slower: the
@@ -80,31 +96,41 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_large_kernel(
   const int high = min(8, tiles_m - 8 * grp);
   const int m0 = (8 * grp + in % high) * T::BM, n0 = (in / high) * T::BN;
   const int steps = K >> 7;
+  const int mine = (steps - wk + WK - 1) / WK, turns = (steps + WK - 1) / WK;   // steps wk, wk + WK, ...
+  uint8_t* lds = lds_all + wk * 2 * T::STEP;
 
   // ---- copies: units of 8 rows, weights first.  N % 16 == 0, so a unit of
   // weight rows is whole or past the end (then the last one is repeated);
   // token rows past M repeat the last row, lane by lane.
   const int u0 = wave * UNITS;
-  const bool wside = u0 < T::BN / 8;
   const int r8 = lane >> 3, slot = lane & 7;
   // weights: slot ^ (2 (u % 4) + r8 bit 1); tokens: slot ^ (4 (u % 2) + r8 / 2)
-  const int f0 = wside ? (r8 >> 1) & 1 : r8 >> 1;
-  const uint32_t voff = (uint32_t)r8 * (uint32_t)K + 16u * (slot ^ f0);
-  const int edge = wside ? 7 : max(min(7, M - 1 - m0 - ((M - 1 - m0) & ~7)), 0);   // last row of the last unit
-  const uint32_t voff_edge = (uint32_t)min(r8, edge) * (uint32_t)K + 16u * (slot ^ f0);
-  const int last_unit = wside ? (N - n0) / 8 - 1 : (M - 1 - m0) >> 3;
-  const uint8_t* base = wside ? wq + (size_t)n0 * K : xq + (size_t)m0 * K;
+  const uint32_t voff_w = (uint32_t)r8 * (uint32_t)K + 16u * (slot ^ ((r8 >> 1) & 1));
+  const uint32_t voff_t = (uint32_t)r8 * (uint32_t)K + 16u * (slot ^ (r8 >> 1));
+  const uint32_t voff_e = (uint32_t)min(r8, (M - 1 - m0) & 7) * (uint32_t)K + 16u * (slot ^ (r8 >> 1));
+  const int last_w = (N - n0) / 8 - 1, last_t = (M - 1 - m0) >> 3;
+  const uint8_t* wbase = wq + (size_t)n0 * K;
+  const uint8_t* tbase = xq + (size_t)m0 * K;
   const uint32_t lds0 = lds_address(lds);
-  auto copy = [&](int t) __attribute__((always_inline)) {
-    const uint8_t* src = base + (size_t)t * 128;
-    const uint32_t dst = lds0 + (t & 1) * T::STEP + u0 * 1024;
+  // scales: lane l the wave's token l (its 16 MT; the others repeat)
+  const int m_wave = m0 + 16 * MT * wm;
+  const uint8_t* sbase = reinterpret_cast<const uint8_t*>(xs + (size_t)min(m_wave, M - 1) * steps);
+  const uint32_t svoff = (uint32_t)max(min(lane & (16 * MT - 1), M - 1 - m_wave), 0) * (uint32_t)steps * 4u;
+  auto copy = [&](int v) __attribute__((always_inline)) {   // the v-th of this group's steps
+    const int t = v * WK + wk;
+    const uint32_t dst = lds0 + (v & 1) * T::STEP + u0 * 1024;
 #pragma unroll
     for (int j = 0; j < UNITS; ++j) {
-      const int u = wside ? u0 + j : u0 + j - T::BN / 8;
-      const int at = min(u, last_unit);
-      const uint32_t x = wside ? 32u * (u & 3) : 64u * (u & 1);
-      dma_16(src + (size_t)at * 8 * K, (at == last_unit ? voff_edge : voff) ^ x, dst + 1024 * j);
+      const int u = u0 + j;
+      if (u < T::BN / 8) {
+        dma_16(wbase + (size_t)min(u, last_w) * 8 * K + (size_t)t * 128, voff_w ^ (32u * (u & 3)), dst + 1024 * j);
+      } else {
+        const int ut = u - T::BN / 8, at = min(ut, last_t);
+        dma_16(tbase + (size_t)at * 8 * K + (size_t)t * 128, (at == last_t ? voff_e : voff_t) ^ (64u * (ut & 1)),
+               dst + 1024 * j);
+      }
     }
+    dma_4(sbase + (size_t)t * 4, svoff, lds0 + (v & 1) * T::STEP + T::CODES + 256 * wave);
   };
 
   // ---- fragment addresses: chunk g (and, 4 chunks on, g + 4) of the row
@@ -125,26 +151,23 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_large_kernel(
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[nt][mt] = (b4f){0.f, 0.f, 0.f, 0.f};
-
-  // token scales of a step, one per thread, two steps ahead
-  const float* sxp = xs + (size_t)min(m0 + tid, M - 1) * steps;
-  const float* swp = ws + (size_t)((n0 + 16 * NT * wn) >> 7 < (N + 127) >> 7 ? (n0 + 16 * NT * wn) >> 7 : 0) * steps;
-  copy(0);
-  float sx_next = 0.f;
-  if (tid < T::BM) {
-    sxl[0][tid] = sxp[0];
-    sx_next = sxp[min(1, steps - 1)];
-  }
-  for (int t = 0; t < steps; ++t) {
+  const int nb = n0 >> 7;                                   // the block's out-features share a scale block
+  if (mine > 0) copy(0);
+  // the weight scales of all steps; the first barrier below makes them visible
+  for (int i = tid; i < steps; i += 64 * T::WAVES * WK) swl[i] = ws[(size_t)nb * steps + i];
+  for (int v = 0; v < turns; ++v) {
     dma_wait();
     __syncthreads();
-    if (t + 1 < steps) copy(t + 1);
-    if (tid < T::BM) {
-      sxl[(t + 1) & 1][tid] = sx_next;
-      sx_next = sxp[min(t + 2, steps - 1)];
-    }
-    const float sw = swp[t];
-    const uint8_t* buf = lds + (t & 1) * T::STEP;
+    if (v + 1 < mine) copy(v + 1);
+    if (WK > 1 && v >= mine) break;                         // the last turn of a group with one step less
+    const float sw = swl[v * WK + wk];
+    const uint8_t* buf = lds + (v & 1) * T::STEP;
+    const float* sx = reinterpret_cast<const float*>(buf + T::CODES + 256 * wave);
+    b4i blo, bhi;
+    auto read_b = [&](int mt) __attribute__((always_inline)) {
+      blo = *reinterpret_cast<const b4i*>(buf + boff[mt & 1] + (mt >> 1) * 32 * 128);
+      bhi = *reinterpret_cast<const b4i*>(buf + (boff[mt & 1] ^ 64) + (mt >> 1) * 32 * 128);
+    };
     b8bf a[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -155,28 +178,66 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_large_kernel(
       a[nt][2] = widen_codes(hi[0], hi[1]);
       a[nt][3] = widen_codes(hi[2], hi[3]);
     }
+    read_b(0);
+    constexpr int NP = NT / 2;
+    b4f p[2][2];
+    float s_old = 0.f;
+    auto scale_pair = [&](int set, int mt, int pr, float s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[2 * pr + h][mt][i] = fmaf(p[set][h][i], s, acc[2 * pr + h][mt][i]);
+    };
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const b4i lo = *reinterpret_cast<const b4i*>(buf + boff[mt & 1] + (mt >> 1) * 32 * 128);
-      const b4i hi = *reinterpret_cast<const b4i*>(buf + (boff[mt & 1] ^ 64) + (mt >> 1) * 32 * 128);
-      const float s = sxl[t & 1][16 * MT * wm + 16 * mt + l16] * sw;
-      b4f p[NT];
+      const float s = sx[16 * mt + l16] * sw;
+      b8bf b[4];
+      b[0] = widen_codes(blo[0], blo[1]);
+      b[1] = widen_codes(blo[2], blo[3]);
+      b[2] = widen_codes(bhi[0], bhi[1]);
+      b[3] = widen_codes(bhi[2], bhi[3]);
+      if (mt + 1 < MT) read_b(mt + 1);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const b8bf b = x < 2 ? widen_codes(lo[2 * (x & 1)], lo[2 * (x & 1) + 1]) : widen_codes(hi[2 * (x & 1)], hi[2 * (x & 1) + 1]);
+      for (int pr = 0; pr < NP; ++pr) {
+        const int set = (mt * NP + pr) & 1;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          p[nt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[nt][x], b, x ? p[nt] : (b4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            p[set][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[2 * pr + h][x], b[x],
+                                                                x ? p[set][h] : (b4f){0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        if (pr > 0) scale_pair(set ^ 1, mt, pr - 1, s);
+        else if (mt > 0) scale_pair(set ^ 1, mt - 1, NP - 1, s_old);
       }
+      s_old = s;
+    }
+    scale_pair((MT * NP - 1) & 1, MT - 1, NP - 1, s_old);
+  }
+
+  if constexpr (WK > 1) {
+    // groups 1.. hand their sums to group 0, each wave to the wave of its place
+    __syncthreads();
+    b4f* j = reinterpret_cast<b4f*>(lds_all);               // [group][wave][nt][mt][lane]
+    if (wk > 0) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][mt][i] = fmaf(p[nt][i], s, acc[nt][mt][i]);
+        for (int mt = 0; mt < MT; ++mt)
+          j[((((wk - 1) * T::WAVES + wave) * NT + nt) * MT + mt) * 64 + lane] = acc[nt][mt];
     }
-  }
+    __syncthreads();
+    if (wk > 0) return;
 #pragma unroll
-  for (int p2 = 0; p2 < NT / 2; ++p2) {
-    const int n = n0 + 16 * NT * wn + 32 * p2 + 8 * g;
+    for (int k = 0; k < WK - 1; ++k)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) acc[nt][mt] += j[(((k * T::WAVES + wave) * NT + nt) * MT + mt) * 64 + lane];
+  }
+
+#pragma unroll
+  for (int pr = 0; pr < NT / 2; ++pr) {
+    const int n = n0 + 16 * NT * wn + 32 * pr + 8 * g;
     if (n >= N) continue;
     float bv[8];
 #pragma unroll
@@ -184,13 +245,13 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_large_kernel(
     add_bias8<DT>(bias, n, bv);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int m = m0 + 16 * MT * wm + 16 * mt + l16;
+      const int m = m_wave + 16 * mt + l16;
       if (m >= M) continue;
       float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[i] = acc[2 * p2][mt][i] + bv[i];
-        v[4 + i] = acc[2 * p2 + 1][mt][i] + bv[4 + i];
+        v[i] = acc[2 * pr][mt][i] + bv[i];
+        v[4 + i] = acc[2 * pr + 1][mt][i] + bv[4 + i];
       }
       *reinterpret_cast<b4i*>(Y + (size_t)m * N + n) = narrow8<DT>(v);
     }
@@ -199,96 +260,170 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void fp8_large_kernel(
 
 // ------------------------------------------------------------ few tokens
 //
-// The weights are read once for at most 16 MT tokens of a block, so their
-// bytes bound it.  A block owns 16 out-features, its waves take steps of 128 k
-// in turn straight from memory (a row's step is one whole line) and are
+// At most 16 tokens a block, so the weights' bytes bound it (16 x 3072 ->
+// 9216: 12.5 us, 2.3 TB/s; token rows cost as many line accesses as weight
+// rows).  A block owns 16 out-features; its 8 waves take steps of 128 k in turn
+// straight from memory to registers (a row's step is one whole line) and are
 // joined in LDS.
 
-template <int DT, int MT>
+template <int DT>
 __global__ __launch_bounds__(512) void fp8_few_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs,
                                                       const uint8_t* __restrict__ wq, const float* __restrict__ ws,
                                                       const uint16_t* __restrict__ bias, int M, int K, int N,
                                                       uint16_t* __restrict__ Y) {
   constexpr int WV = 8;
-  __shared__ float red[WV][MT][16][17];
+  __shared__ float red[WV][16][17];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT, steps = K >> 7;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16, steps = K >> 7;
+  const int m = min(m0 + l16, M - 1);
   const uint8_t* ap = wq + (size_t)(n0 + l16) * K + 16 * g;
-  const uint8_t* bp[MT];
-  const float* sx[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int m = min(m0 + 16 * mt + l16, M - 1);
-    bp[mt] = xq + (size_t)m * K + 16 * g;
-    sx[mt] = xs + (size_t)m * steps;
-  }
+  const uint8_t* bp = xq + (size_t)m * K + 16 * g;
+  const float* sx = xs + (size_t)m * steps;
   const float* sw = ws + (size_t)(n0 >> 7) * steps;
-  b4f acc[MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) acc[mt] = (b4f){0.f, 0.f, 0.f, 0.f};
+  b4f acc = (b4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
   for (int t = wave; t < steps; t += WV) {
     const b4i alo = *reinterpret_cast<const b4i*>(ap + 128 * (size_t)t);
     const b4i ahi = *reinterpret_cast<const b4i*>(ap + 128 * (size_t)t + 64);
-    const float w = sw[t];
+    const b4i blo = *reinterpret_cast<const b4i*>(bp + 128 * (size_t)t);
+    const b4i bhi = *reinterpret_cast<const b4i*>(bp + 128 * (size_t)t + 64);
+    const float s = sx[t] * sw[t];
+    b4f p = (b4f){0.f, 0.f, 0.f, 0.f};
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(alo[0], alo[1]), widen_codes(blo[0], blo[1]), p, 0, 0, 0);
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(alo[2], alo[3]), widen_codes(blo[2], blo[3]), p, 0, 0, 0);
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(ahi[0], ahi[1]), widen_codes(bhi[0], bhi[1]), p, 0, 0, 0);
+    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(ahi[2], ahi[3]), widen_codes(bhi[2], bhi[3]), p, 0, 0, 0);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const b4i blo = *reinterpret_cast<const b4i*>(bp[mt] + 128 * (size_t)t);
-      const b4i bhi = *reinterpret_cast<const b4i*>(bp[mt] + 128 * (size_t)t + 64);
-      b4f p = (b4f){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(alo[2 * x], alo[2 * x + 1]), widen_codes(blo[2 * x], blo[2 * x + 1]), p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_codes(ahi[2 * x], ahi[2 * x + 1]), widen_codes(bhi[2 * x], bhi[2 * x + 1]), p, 0, 0, 0);
-      }
-      const float s = sx[mt][t] * w;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[mt][i] = fmaf(p[i], s, acc[mt][i]);
-    }
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(p[i], s, acc[i]);
   }
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][mt][l16][4 * g + i] = acc[mt][i];
+  for (int i = 0; i < 4; ++i) red[wave][l16][4 * g + i] = acc[i];
   __syncthreads();
-  for (int o = threadIdx.x; o < MT * 256; o += 512) {
-    const int mt = o >> 8, r = (o >> 4) & 15, c = o & 15, m = m0 + 16 * mt + r;
+  if (threadIdx.x < 256) {
+    const int r = threadIdx.x >> 4, c = threadIdx.x & 15;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WV; ++w) v += red[w][mt][r][c];
-    if (m < M) {
+    for (int w = 0; w < WV; ++w) v += red[w][r][c];
+    if (m0 + r < M) {
       if (bias) v += widen2<DT>(bias[n0 + c])[0];
-      Y[(size_t)m * N + n0 + c] = (uint16_t)narrow2<DT>(v, 0.f);
+      Y[(size_t)(m0 + r) * N + n0 + c] = (uint16_t)narrow2<DT>(v, 0.f);
     }
   }
 }
 
+// ------------------------------------------------------------- one token
+//
+// No matrix unit: a wave reads RW weight rows 1 KB at a time (whole lines, 16
+// codes a lane), multiplies them with the token's codes of the same places and
+// keeps one fp32 sum per row and lane; a lane's codes of a kilobyte lie in one
+// scale block.  The lanes are added at the end.  3072 -> 9216: 7.4 us, 3.8 TB/s.
+
+template <int DT, int RW>
+__global__ __launch_bounds__(256) void fp8_row_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs,
+                                                      const uint8_t* __restrict__ wq, const float* __restrict__ ws,
+                                                      const uint16_t* __restrict__ bias, int K, int N,
+                                                      uint16_t* __restrict__ Y) {
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = (blockIdx.x * 4 + wave) * RW, steps = K >> 7;
+  if (n0 >= N) return;
+  const uint8_t* wp = wq + (size_t)n0 * K;
+  const float* sw = ws + (size_t)(n0 >> 7) * steps;
+  float acc[RW];
+#pragma unroll
+  for (int r = 0; r < RW; ++r) acc[r] = 0.f;
+#pragma unroll 4
+  for (int k = 16 * lane; k < K; k += 1024) {
+    b4i w[RW];
+#pragma unroll
+    for (int r = 0; r < RW; ++r) w[r] = *reinterpret_cast<const b4i*>(wp + (size_t)r * K + k);
+    const b4i c = *reinterpret_cast<const b4i*>(xq + k);
+    const float s = xs[k >> 7] * sw[k >> 7];
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const b2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(c[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(c[i], true);
+      x[4 * i] = lo[0] * s;
+      x[4 * i + 1] = lo[1] * s;
+      x[4 * i + 2] = hi[0] * s;
+      x[4 * i + 3] = hi[1] * s;
+    }
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const b2f lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[r][i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[r][i], true);
+        acc[r] = fmaf(lo[0], x[4 * i], acc[r]);
+        acc[r] = fmaf(lo[1], x[4 * i + 1], acc[r]);
+        acc[r] = fmaf(hi[0], x[4 * i + 2], acc[r]);
+        acc[r] = fmaf(hi[1], x[4 * i + 3], acc[r]);
+      }
+  }
+#pragma unroll
+  for (int r = 0; r < RW; ++r) {
+#pragma unroll
+    for (int d = 32; d; d >>= 1) acc[r] += __shfl_xor(acc[r], d);
+    if (lane == 0) {
+      const float v = acc[r] + (bias ? widen2<DT>(bias[n0 + r])[0] : 0.f);
+      Y[n0 + r] = (uint16_t)narrow2<DT>(v, 0.f);
+    }
+  }
+}
+
+// The variant of a call, by its sizes.  Tiles are taken as large as the chip
+// can still be filled with (256 compute units), and where they are few, waves
+// take the steps of k in turn.  Measured, us (tile side or sides, groups):
+//   M x K x N          row   few   32/8  32x64/4  64/4   64/2   128/1
+//   1 x 3072 x 9216    7.4   8.4                  12.3
+//   16 x 3072 x 9216         12.5  13.4           12.5
+//   64 x 1024 x 1024         3.1   4.3            6.7    6.0    12.1
+//   64 x 12288 x 3072        41    17     27      37     43     115
+//   128 x 12288 x 3072       80    32     27      36     43     116
+//   64 x 3072 x 9216         32    18     18      12.8   13.7   32
+//   256 x 3072 x 3072        42    17     17      12.5   13.5   32
+//   333 x 12288 x 3072       208   78     78      73     66     115
+//   512 x 4096 x 4096        141   50     39      30     28     41
+//   1024 x 3072 x 9216       469   184    136     98     82     72
+//   4096 x 3072 x 9216                                   311    214
 template <int DT>
 svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const uint16_t* bias,
                        int M, int K, int N, uint16_t* Y, hipStream_t st) {
-  auto large = [&](auto nt, auto mt, auto wn, auto wm) {
-    using T = LargeTile<decltype(nt)::value, decltype(mt)::value, decltype(wn)::value, decltype(wm)::value>;
-    const int tm = (M + T::BM - 1) / T::BM, tn = (N + T::BN - 1) / T::BN;
-    hipLaunchKernelGGL((fp8_large_kernel<DT, decltype(nt)::value, decltype(mt)::value, decltype(wn)::value, decltype(wm)::value>),
-                       dim3(tm * tn), dim3(64 * T::WAVES), 0, st, xq, xs, wq, ws, bias, M, K, N, Y, tm, tn);
-  };
   using std::integral_constant;
+  typedef integral_constant<int, 1> I1;
   typedef integral_constant<int, 2> I2;
   typedef integral_constant<int, 4> I4;
   typedef integral_constant<int, 8> I8;
-  const int64_t t256 = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-  const int64_t t128 = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
-  if (M <= 64) {
-    if (M <= 16) hipLaunchKernelGGL((fp8_few_kernel<DT, 1>), dim3(N / 16, 1), dim3(512), 0, st, xq, xs, wq, ws, bias, M, K, N, Y);
-    else hipLaunchKernelGGL((fp8_few_kernel<DT, 2>), dim3(N / 16, (M + 31) / 32), dim3(512), 0, st, xq, xs, wq, ws, bias, M, K, N, Y);
-  } else if (t256 >= 256) {
-    large(I4{}, I8{}, I4{}, I2{});
-  } else if (t128 >= 200) {
-    large(I4{}, I4{}, I2{}, I2{});
+  auto blocks = [&](int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  auto row = [&](auto rw) {
+    constexpr int RW = decltype(rw)::value;
+    hipLaunchKernelGGL((fp8_row_kernel<DT, RW>), dim3((N / RW + 3) / 4), dim3(256), 0, st, xq, xs, wq, ws, bias, K, N, Y);
+  };
+  auto tile = [&](auto nt, auto mt, auto wn, auto wm, auto wk) {   // two buffers per group
+    constexpr int NT = decltype(nt)::value, MT = decltype(mt)::value, WN = decltype(wn)::value,
+                  WM = decltype(wm)::value, WK = decltype(wk)::value;
+    using T = Tile<NT, MT, WN, WM, WK>;
+    const int tm = (M + T::BM - 1) / T::BM, tn = (N + T::BN - 1) / T::BN;
+    hipLaunchKernelGGL((fp8_tile_kernel<DT, NT, MT, WN, WM, WK>), dim3(tm * tn), dim3(64 * T::WAVES * WK), 0, st,
+                       xq, xs, wq, ws, bias, M, K, N, Y, tm, tn);
+  };
+  if (M == 1) {
+    if (N >= 6144) row(I2{});   // 3072 -> 9216: 7.3 us against 7.7 with one row; 12288 -> 3072: 9.1 against 8.4
+    else row(I1{});
+  } else if (M <= 16 || blocks(16, 16) <= 256) {
+    hipLaunchKernelGGL((fp8_few_kernel<DT>), dim3(N / 16, (M + 15) / 16), dim3(512), 0, st, xq, xs, wq, ws, bias, M, K,
+                       N, Y);
+  } else if (blocks(32, 32) <= 256) {
+    tile(I2{}, I2{}, I1{}, I1{}, I8{});
+  } else if (blocks(64, 32) <= 256) {
+    tile(I2{}, I2{}, I1{}, I2{}, I4{});
+  } else if (blocks(64, 64) <= 256) {
+    tile(I2{}, I2{}, I2{}, I2{}, I4{});
+  } else if (blocks(64, 64) <= 1280) {
+    tile(I2{}, I2{}, I2{}, I2{}, I2{});
   } else {
-    large(I2{}, I2{}, I2{}, I2{});
+    tile(I4{}, I4{}, I2{}, I2{}, I1{});
   }
   return launched();
 }
