@@ -464,7 +464,7 @@ typedef struct svdq_attention_args {
   float scale;                  /* of q . k */
   float softcap;                /* > 0: scores become softcap * tanh(score / softcap); 0: off */
   /* device, element (b, i, h, d) at b * batch + i * token + h * head + d;
-   * strides are multiples of 8 elements, k_token and v_token in 0..2^28.  k and
+   * strides are multiples of 8 elements, k_token and v_token in 0..2^25.  k and
    * v may be NULL if Skv == 0.  B Hq Sq is at most 2^30. */
   const uint16_t *q, *k, *v;
   uint16_t* o;

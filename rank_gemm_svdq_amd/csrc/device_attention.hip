@@ -31,6 +31,15 @@
 // buffers and no barriers, and are joined at the end.  Where blocks are few,
 // the keys are split over blocks too; a second kernel joins the parts.
 //
+// What bounds it.  Many rows: power and the serial chain of a wave's tile
+// (scores 700 cycles, maximum 440, weights 740, values 800 and 560 for the
+// barrier and the copies, two waves a SIMD, at 1.6 - 1.8 GHz under this load):
+// 4608 tokens x 24 heads of 128: 297 us, 880 TFLOP/s; causal 154 us.  64 rows a
+// wave with the two row tiles' softmax and MFMAs side by side (one wave a
+// SIMD) took 525 us, eight waves sharing the copies half a tile apart 345 us.
+// One token: the bytes of K and V; 16 requests of 4096 - 16384 keys x 8 heads
+// 132 us, 5.1 TB/s.
+//
 // Hidden keys.  A hidden score is -infinity, its weight 0, and 0 times what V
 // holds there would be NaN if that is not finite.  O is checked at the end:
 // rows that came out not finite are computed again key by key, without the
@@ -41,6 +50,7 @@
 namespace svdq {
 namespace {
 
+constexpr int kSeen = 2048;  // tiles of a block looked through for their documents
 constexpr int kCus = 256;   // compute units of the chip, for the host-side choice of splits
 
 struct Part {               // how the keys are split over blocks
@@ -75,6 +85,33 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Which (entry, K/V head) and which of its row tiles and key parts a block
+// takes.  Blocks are dealt to the 8 XCDs round robin; with a multiple of 8
+// groups an XCD keeps to groups of its own, so that its L2 holds their K and V.
+// Neighbouring blocks take different groups: the rows of one head lie a fixed
+// stride apart, which can put them all on a few of the L2's channels (4608
+// tokens x 24 heads of 128: 350 us with one group after the other, 317 us
+// so), and the longest rows of a causal mask then come first in every group
+// (237 against 178 us).
+template <bool KEYS>
+__device__ __forceinline__ void group_order(const AttnP& p, int* grp, int* rest) {
+  const int b = blockIdx.x;
+  if constexpr (KEYS) {
+    // nothing is shared between blocks: the parts of a group follow each other
+    // (one token of 16 requests: 142 us, 150 the other way)
+    const int id = xcd_order(b, gridDim.x), per = p.tiles * p.part.splits;
+    *grp = id / per;
+    *rest = id % per;
+  } else if ((p.groups & 7) == 0) {
+    const int own = p.groups >> 3, i = b >> 3;
+    *grp = (b & 7) * own + i % own;
+    *rest = i / own;
+  } else {
+    *grp = b % p.groups;
+    *rest = b / p.groups;
+  }
+}
 
 // Score in powers of two of a raw dot product (times scale > 0, cap and bias).
 __device__ __forceinline__ float capped(const AttnP& p, float s) {
@@ -123,6 +160,69 @@ __device__ __forceinline__ void row_again(const AttnP& p, int b, int hk, int r, 
   *o_out = o;
 }
 
+// The end of 32 rows of a wave (lane l: row row0 + l % 32, O^T as the MFMAs
+// leave it, m and l of the whole row): rows that are not finite are computed
+// again over keys [j0, j1), the others stored, as parts or finished.
+template <int DT, int DP, bool PAD>
+__device__ __forceinline__ void store_rows(const AttnP& p, int grp, int b, int hk, int sp, int n, int row0, int j0,
+                                           int j1, float m, float l, const b16f (&o)[DP / 32]) {
+  const svdq_attention_args& a = p.a;
+  constexpr int ND = DP / 32;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  const int row = min(row0 + l32, p.R - 1);
+  bool bad = !(fabsf(l) < __builtin_inff());
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) bad = bad || !(fabsf(o[d][i]) < __builtin_inff());
+  const bool real = row0 + l32 < p.R;
+  const uint64_t who = __ballot(bad && real);
+  const uint32_t again = (uint32_t)(who | (who >> 32));
+  const size_t rows_all = (size_t)p.groups * p.R;
+  const bool parts = p.part.splits > 1;
+  if (real && !((again >> l32) & 1)) {
+    if (parts) {
+      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + row;
+      float* op = p.part.o + at * DP;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<b4f*>(op + 32 * d + 8 * g + 4 * half) =
+              (b4f){o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+      if (half == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(m, l);
+    } else {
+      const float by = l != 0.f ? 1.0f / l : 0.f;
+      const int qi = row / p.G, qh = hk * p.G + row % p.G;
+      uint16_t* op = a.o + b * a.o_batch + qi * a.o_token + qh * a.o_head;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int at = 32 * d + 8 * g + 4 * half;
+          if (!PAD || at < a.D)
+            *reinterpret_cast<uint2*>(op + at) = make_uint2(narrow2<DT>(o[d][4 * g] * by, o[d][4 * g + 1] * by),
+                                                            narrow2<DT>(o[d][4 * g + 2] * by, o[d][4 * g + 3] * by));
+        }
+    }
+  }
+  for (uint32_t left = again; left; left &= left - 1) {
+    const int r = row0 + __builtin_ctz(left);
+    float rm, rl;
+    b2f ro;
+    row_again<DT>(p, b, hk, r, n, j0, j1, &rm, &rl, &ro);
+    if (parts) {
+      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + r;
+      if (2 * lane < DP) *reinterpret_cast<b2f*>(p.part.o + at * DP + 2 * lane) = ro;
+      if (lane == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(rm, rl);
+    } else if (2 * lane < a.D) {
+      const float by = rl != 0.f ? 1.0f / rl : 0.f;
+      uint16_t* op = a.o + b * a.o_batch + (r / p.G) * a.o_token + (hk * p.G + r % p.G) * a.o_head;
+      *reinterpret_cast<uint32_t*>(op + 2 * lane) = narrow2<DT>(ro[0] * by, ro[1] * by);
+    }
+  }
+}
+
 // KEYS: waves share 32 rows and take key tiles in turn; otherwise waves take
 // rows and share key tiles.  PAD: D < DP.
 template <int DT, int DP, bool PAD, bool KEYS>
@@ -138,17 +238,18 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
   constexpr int MINE = KEYS ? COPIES : COPIES / 4; // per wave
   constexpr int NS = DP / 16;                      // MFMA steps of S
   constexpr int ND = DP / 32;                      // 32-column tiles of O
+  constexpr int AHEAD_K = 4, AHEAD_V = 2;        // fragments read ahead
   constexpr int RING = 4 * TILE;                   // K, V of two tiles
   constexpr int LDS = KEYS ? 4 * RING : RING;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   __shared__ int docs[4][TK];
+  __shared__ uint32_t seen[KEYS ? 1 : kSeen / 32];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, half = lane >> 5;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
-  const int per_group = p.tiles * p.part.splits;
-  const int grp = id / per_group, rest = id % per_group;
+  int grp, rest;
+  group_order<KEYS>(p, &grp, &rest);
   // the last rows see most keys under a causal mask: they go first
   const int rt = p.tiles - 1 - rest / p.part.splits, sp = rest % p.part.splits;
   const int b = grp / a.Hkv, hk = grp % a.Hkv;
@@ -190,16 +291,13 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     }
   }
   const int qd = use_docs ? a.q_doc[(size_t)b * a.Sq + qi] : 0;
-  int doc_lo = 0, doc_hi = 0;   // of the rows of the block (rows arrangement) or the wave
-  if (use_docs) {
-    doc_lo = doc_hi = qd;
-    if constexpr (!KEYS) {
+  int doc_lo = qd, doc_hi = qd;   // documents of the block's rows
+  if (!KEYS && use_docs) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int d = a.q_doc[(size_t)b * a.Sq + min(row_base + 64 * k + lane, p.R - 1) / p.G];
-        doc_lo = min(doc_lo, d);
-        doc_hi = max(doc_hi, d);
-      }
+    for (int k = 0; k < 2; ++k) {
+      const int d = a.q_doc[(size_t)b * a.Sq + min(row_base + 64 * k + lane, p.R - 1) / p.G];
+      doc_lo = min(doc_lo, d);
+      doc_hi = max(doc_hi, d);
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) {
@@ -224,27 +322,37 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
   // chunk of K row r at slot c and the other way round
   auto k_chunk = [&](int r, int c) { return DP == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7); };
   auto v_chunk = [&](int r, int c) { return DP == 128 ? c ^ (4 * (r & 3)) : c ^ (4 * ((r >> 1) & 1)); };
-  const uint64_t kst = 2 * (uint64_t)a.k_token, vst = 2 * (uint64_t)a.v_token;
+  const uint32_t kst = 2u * (uint32_t)a.k_token, vst = 2u * (uint32_t)a.v_token;   // at most 2^26
+  const int r_first = RPI * (KEYS ? 0 : MINE * wave);
+  uint32_t koffs[MINE], voffs[MINE];
+  bool klive[MINE], vlive[MINE];
+#pragma unroll
+  for (int c = 0; c < MINE; ++c) {
+    const int r = r_first + RPI * c + crow, kc = k_chunk(r, cslot), vc = v_chunk(r, cslot);
+    koffs[c] = (uint32_t)r * kst + 16 * kc;
+    voffs[c] = (uint32_t)r * vst + 16 * vc;
+    klive[c] = !PAD || 8 * kc < a.D;
+    vlive[c] = !PAD || 8 * vc < a.D;
+  }
   auto copy_tile = [&](int t, int buf) __attribute__((always_inline)) {
-    const int j0 = t * TK, last = n - 1 - j0;      // rows past the last key in use repeat it
+    const uint8_t *kp = kbase + (uint64_t)(t * TK) * kst, *vp = vbase + (uint64_t)(t * TK) * vst;
+    const uint32_t dst = lbase + buf * 2 * TILE + r_first * ROWB;
+    const int last = n - 1 - t * TK;
+    if (last >= TK - 1) {
 #pragma unroll
-    for (int c = 0; c < MINE; ++c) {
-      const int r0 = RPI * (KEYS ? c : MINE * wave + c);
-      const int from = min(r0, last);
-      const uint32_t dr = (uint32_t)(min(r0 + crow, last) - from);
-      const int kc = k_chunk(r0 + crow, cslot);
-      if (!PAD || 8 * kc < a.D)
-        dma_16(kbase + (uint64_t)(j0 + from) * kst, dr * (uint32_t)kst + 16 * kc, lbase + buf * 2 * TILE + RPI * ROWB * (KEYS ? c : MINE * wave + c));
-    }
+      for (int c = 0; c < MINE; ++c) {
+        if (klive[c]) dma_16(kp, koffs[c], dst + 1024 * c);
+        if (vlive[c]) dma_16(vp, voffs[c], dst + TILE + 1024 * c);
+      }
+    } else {
+      // the last tile: rows past the last key in use repeat it
 #pragma unroll
-    for (int c = 0; c < MINE; ++c) {
-      const int r0 = RPI * (KEYS ? c : MINE * wave + c);
-      const int from = min(r0, last);
-      const uint32_t dr = (uint32_t)(min(r0 + crow, last) - from);
-      const int vc = v_chunk(r0 + crow, cslot);
-      if (!PAD || 8 * vc < a.D)
-        dma_16(vbase + (uint64_t)(j0 + from) * vst, dr * (uint32_t)vst + 16 * vc,
-               lbase + buf * 2 * TILE + TILE + RPI * ROWB * (KEYS ? c : MINE * wave + c));
+      for (int c = 0; c < MINE; ++c) {
+        const int r = r_first + RPI * c + crow;
+        const uint32_t over = (uint32_t)max(r - last, 0);
+        if (klive[c]) dma_16(kp, koffs[c] - over * kst, dst + 1024 * c);
+        if (vlive[c]) dma_16(vp, voffs[c] - over * vst, dst + TILE + 1024 * c);
+      }
     }
   };
 
@@ -268,19 +376,59 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
 
   const bool plain = !(a.softcap > 0.f) && !a.slopes;   // score = c1 x dot product
 
-  // kd: document of key j0 + lane (where documents are used)
-  auto compute = [&](int t, int buf, int kd) __attribute__((always_inline)) {
+  b4i pf[2 * KT];   // weights of a tile, 16 bits
+
+  // O += V P of the tile in `buf`, fragments AHEAD_V MFMAs ahead (the first of
+  // them are read before the weights are worked out)
+  b4i vf[AHEAD_V];
+  auto read_v = [&](int buf, int i) __attribute__((always_inline)) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    const uint8_t* vl = wl + buf * 2 * TILE + TILE + voff[i % ND] + 16 * (i / ND) * ROWB;
+    const s4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SVDQ_LDS s4*)vl);
+    const s4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SVDQ_LDS s4*)(vl + 8 * ROWB));
+    const int2 lo = __builtin_bit_cast(int2, v0), hi = __builtin_bit_cast(int2, v1);
+    vf[i % AHEAD_V] = (b4i){lo.x, lo.y, hi.x, hi.y};
+  };
+  auto first_values = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < AHEAD_V; ++i) read_v(buf, i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto values = [&](int buf) __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 2 * KT * ND; ++i) {
+      o[i % ND] = mma<DT>(vf[i % AHEAD_V], pf[i / ND], o[i % ND]);
+      if (i + AHEAD_V < 2 * KT * ND) read_v(buf, i + AHEAD_V);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // Scores and weights of tile t, and the running maximum and sum.  kd:
+  // document of key j0 + lane (where documents are used).
+  auto scores = [&](int t, int buf, int kd) __attribute__((always_inline)) {
     const int j0 = t * TK;
     const uint8_t* kl = wl + buf * 2 * TILE;
-    const uint8_t* vl = kl + TILE;
     b16f s[KT];
 #pragma unroll
-    for (int k = 0; k < KT; ++k) {
+    for (int k = 0; k < KT; ++k)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[k][i] = 0.f;
+    // Consecutive MFMAs add to different registers, and fragments are read
+    // AHEAD_K MFMAs ahead: left to itself the compiler puts each read right
+    // before its MFMA and waits for it, hence the fences.
+    b4i kf[AHEAD_K];
+    auto read_k = [&](int i) __attribute__((always_inline)) {
+      kf[i % AHEAD_K] = *reinterpret_cast<const b4i*>(kl + koff[i / KT] + (i % KT) * 32 * ROWB);
+    };
 #pragma unroll
-      for (int x = 0; x < NS; ++x)
-        s[k] = mma<DT>(*reinterpret_cast<const b4i*>(kl + koff[x] + k * 32 * ROWB), qf[x], s[k]);
+    for (int i = 0; i < AHEAD_K; ++i) read_k(i);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < KT * NS; ++i) {
+      s[i % KT] = mma<DT>(kf[i % AHEAD_K], qf[i / KT], s[i % KT]);
+      if (i + AHEAD_K < KT * NS) read_k(i + AHEAD_K);
+      __builtin_amdgcn_sched_barrier(0);
     }
     float c = p.c1;
     if (!plain) {
@@ -342,7 +490,7 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= f;
     }
-    b4i pf[2 * KT];
+    first_values(buf);
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       float part = 0.f;
@@ -355,16 +503,6 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
 #pragma unroll
       for (int x = 0; x < 8; ++x) pf[2 * k + x / 4][x % 4] = (int)narrow2<DT>(s[k][2 * x], s[k][2 * x + 1]);
     }
-    typedef short s4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int x = 0; x < 2 * KT; ++x) {
-        const s4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SVDQ_LDS s4*)(vl + voff[d] + 16 * x * ROWB));
-        const s4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SVDQ_LDS s4*)(vl + voff[d] + (16 * x + 8) * ROWB));
-        const int2 lo = __builtin_bit_cast(int2, v0), hi = __builtin_bit_cast(int2, v1);
-        o[d] = mma<DT>((b4i){lo.x, lo.y, hi.x, hi.y}, pf[x], o[d]);
-      }
   };
   auto doc_of = [&](int t) -> int {
     return use_docs && t < t_end ? a.k_doc[(size_t)b * a.Skv + min(t * TK + (lane & (TK - 1)), n - 1)] : 0;
@@ -380,52 +518,62 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
       __builtin_amdgcn_wave_barrier();
       if (t + 4 < t_end) copy_tile(t + 4, buf ^ 1);
       const int kd_next = doc_of(t + 4);
-      compute(t, buf, kd);
+      scores(t, buf, kd);
+      values(buf);
       // this tile's LDS reads end before the next copy may overwrite it
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       kd = kd_next;
     }
   } else {
-    // tiles in turn; where documents are used, those that hold none of the
-    // block's are passed over (32 tiles are looked through at a time)
-    int group = -1;
+    // Tiles in turn; where documents are used, those that hold none of the
+    // block's are passed over: the waves look through the first kSeen tiles of
+    // the block's share beforehand (later ones are all visited).
+    if (use_docs) {
+      for (int w = wave; w < (min(t_end - t_begin, kSeen) + 31) / 32; w += 4) {
+        int kd[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int j = (t_begin + 32 * w + k) * TK + lane;
+          kd[k] = a.k_doc[(size_t)b * a.Skv + min(j, n - 1)];
+        }
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) bits |= (__any(kd[k] >= doc_lo && kd[k] <= doc_hi) ? 1u : 0u) << k;
+        if (lane == 0) seen[w] = bits;
+      }
+      __syncthreads();
+    }
+    int word = -1;
     uint32_t bits = 0;
     auto next = [&](int t) -> int {
       if (!use_docs) return t;
-      while (t < t_end) {
-        if (t >> 5 != group) {
-          group = t >> 5;
-          bits = 0;
-#pragma unroll 8
-          for (int k = 0; k < 32; ++k) {
-            const int j = (32 * group + k) * TK + lane;
-            const int kd = j < n ? a.k_doc[(size_t)b * a.Skv + j] : 0;
-            bits |= (__any(j < n && kd >= doc_lo && kd <= doc_hi) ? 1u : 0u) << k;
-          }
+      for (int i = t - t_begin; i < t_end - t_begin && i < kSeen; i = (i | 31) + 1) {
+        if (i >> 5 != word) {
+          word = i >> 5;
+          bits = __builtin_amdgcn_readfirstlane(seen[word]);
         }
-        const uint32_t left = bits >> (t & 31);
-        if (left) return min(t_end, t + __builtin_ctz(left));
-        t = (t | 31) + 1;
+        const uint32_t left = bits >> (i & 31);
+        if (left) return min(t_end, t_begin + i + __builtin_ctz(left));
       }
-      return t_end;
+      return min(t_end, max(t, t_begin + kSeen));
     };
-    int t = next(t_begin);
+    int t = next(t_begin), buf = 0;
     if (t < t_end) copy_tile(t, 0);
     int kd = doc_of(t);
-    auto step = [&](int buf) __attribute__((always_inline)) {
+    while (t < t_end) {
+      // tile t has landed for every wave, and all are done with the one before
       dma_wait();
       __syncthreads();
       const int tn = next(t + 1);
       if (tn < t_end) copy_tile(tn, buf ^ 1);
       const int kd_next = doc_of(tn);
-      if (t * TK < lim_last) compute(t, buf, kd);
+      if (t * TK < lim_last) {
+        scores(t, buf, kd);
+        values(buf);
+      }
       kd = kd_next;
       t = tn;
-    };
-    while (t < t_end) {
-      step(0);
-      if (t >= t_end) break;
-      step(1);
+      buf ^= 1;
     }
   }
 
@@ -476,85 +624,57 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     m = up;
   }
 
-  // ---- rows that are not finite are computed again, the others stored
-  bool bad = !(fabsf(l) < __builtin_inff());
-#pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) bad = bad || !(fabsf(o[d][i]) < __builtin_inff());
-  const bool real = row0 + l32 < p.R;
-  const uint64_t who = __ballot(bad && real);
-  const uint32_t again = (uint32_t)(who | (who >> 32));
-  const size_t rows_all = (size_t)p.groups * p.R;
-  const bool parts = p.part.splits > 1;
-  if (real && !((again >> l32) & 1)) {
-    if (parts) {
-      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + row;
-      float* op = p.part.o + at * DP;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<b4f*>(op + 32 * d + 8 * g + 4 * half) =
-              (b4f){o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
-      if (half == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(m, l);
-    } else {
-      const float by = l != 0.f ? 1.0f / l : 0.f;
-      uint16_t* op = a.o + b * a.o_batch + qi * a.o_token + qh * a.o_head;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int at = 32 * d + 8 * g + 4 * half;
-          if (!PAD || at < a.D)
-            *reinterpret_cast<uint2*>(op + at) = make_uint2(narrow2<DT>(o[d][4 * g] * by, o[d][4 * g + 1] * by),
-                                                            narrow2<DT>(o[d][4 * g + 2] * by, o[d][4 * g + 3] * by));
-        }
-    }
-  }
-  for (uint32_t left = again; left; left &= left - 1) {
-    const int r = row0 + __builtin_ctz(left);
-    float rm, rl;
-    b2f ro;
-    row_again<DT>(p, b, hk, r, n, t_begin * TK, min(n, t_end * TK), &rm, &rl, &ro);
-    if (parts) {
-      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + r;
-      if (2 * lane < DP) *reinterpret_cast<b2f*>(p.part.o + at * DP + 2 * lane) = ro;
-      if (lane == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(rm, rl);
-    } else if (2 * lane < a.D) {
-      const float by = rl != 0.f ? 1.0f / rl : 0.f;
-      uint16_t* op = a.o + b * a.o_batch + (r / p.G) * a.o_token + (hk * p.G + r % p.G) * a.o_head;
-      *reinterpret_cast<uint32_t*>(op + 2 * lane) = narrow2<DT>(ro[0] * by, ro[1] * by);
-    }
-  }
+  store_rows<DT, DP, PAD>(p, grp, b, hk, sp, n, row0, t_begin * TK, min(n, t_end * TK), m, l, o);
 }
 
-// Joins the parts of a row: a quarter wave (16 lanes) per row, 8 elements a lane.
+// Joins the parts of the rows: DP / 8 lanes hold a row's 8-element pieces, and
+// `across` such lane sets (1, 2, .. 16) of a block share the row's parts, so that
+// many parts are a few rounds of loads.
 template <int DT, int DP>
-__global__ __launch_bounds__(256) void join_kernel(AttnP p) {
+__global__ __launch_bounds__(256) void join_kernel(AttnP p, int across) {
   const svdq_attention_args& a = p.a;
   constexpr int LPR = DP / 8;
+  __shared__ float part[256][11];   // 8 sums, maximum, sum of weights; 11: odd stride
   const size_t rows = (size_t)p.groups * p.R;
-  const size_t at = (size_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
-  const int d = 8 * (threadIdx.x % LPR);
-  if (at >= rows || d >= a.D) return;
-  float top = kLow;
-  for (int s = 0; s < p.part.splits; ++s) top = fmaxf(top, p.part.ml[2 * (s * rows + at)]);
-  float sum = 0.f, o[8];
+  const int set = threadIdx.x / LPR, g = set % across, d = 8 * (threadIdx.x % LPR);
+  const size_t at = (size_t)blockIdx.x * (256 / LPR / across) + set / across;
+  const bool live = at < rows;
+  float top = kLow, sum = 0.f, o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int s = 0; s < p.part.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part.ml + 2 * (s * rows + at));
-    const float f = exp2_(ml.x - top);
-    sum = fmaf(f, ml.y, sum);
-    const float* op = p.part.o + (s * rows + at) * DP + d;
-    const b4f x = *reinterpret_cast<const b4f*>(op), y = *reinterpret_cast<const b4f*>(op + 4);
+  if (live) {
+    for (int s = g; s < p.part.splits; s += across) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part.ml + 2 * (s * rows + at));
+      const float* op = p.part.o + (s * rows + at) * DP + d;
+      const b4f x = *reinterpret_cast<const b4f*>(op), y = *reinterpret_cast<const b4f*>(op + 4);
+      const float up = fmaxf(top, ml.x), f0 = exp2_(top - up), f = exp2_(ml.x - up);
+      sum = fmaf(f, ml.y, sum * f0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[i] = fmaf(f, x[i], o[i]);
-      o[4 + i] = fmaf(f, y[i], o[4 + i]);
+      for (int i = 0; i < 4; ++i) {
+        o[i] = fmaf(f, x[i], o[i] * f0);
+        o[4 + i] = fmaf(f, y[i], o[4 + i] * f0);
+      }
+      top = up;
     }
   }
+  if (across > 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = o[i];
+    part[threadIdx.x][8] = top;
+    part[threadIdx.x][9] = sum;
+    __syncthreads();
+    if (g == 0) {
+      for (int k = 1; k < across; ++k) {
+        const float* x = part[threadIdx.x + k * LPR];
+        const float up = fmaxf(top, x[8]), f0 = exp2_(top - up), f = exp2_(x[8] - up);
+        sum = fmaf(f, x[9], sum * f0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(f, x[i], o[i] * f0);
+        top = up;
+      }
+    }
+  }
+  if (!live || g != 0 || d >= a.D) return;
   const float by = sum != 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] *= by;
@@ -580,7 +700,7 @@ svdq_status check(const svdq_attention_args* a) {
                         a->v_batch, a->v_token, a->v_head, a->o_batch, a->o_token, a->o_head};
   for (int64_t s : st)
     if (s % 8 != 0) return SVDQ_ERR_ALIGN;
-  if (a->k_token < 0 || a->v_token < 0 || a->k_token > (1 << 28) || a->v_token > (1 << 28)) return SVDQ_ERR_SHAPE;
+  if (a->k_token < 0 || a->v_token < 0 || a->k_token > (1 << 25) || a->v_token > (1 << 25)) return SVDQ_ERR_SHAPE;
   if (!on16(a->q) || !on16(a->k) || !on16(a->v) || !on16(a->o) || !on4(a->slopes) || !on4(a->kv_len) ||
       !on4(a->prefix) || !on4(a->q_doc) || !on4(a->k_doc))
     return SVDQ_ERR_ALIGN;
@@ -602,8 +722,10 @@ Plan plan_of(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_
   p.keys = p.R <= 32;
   p.tiles = p.keys ? 1 : (p.R + 127) / 128;
   const int64_t blocks = (int64_t)p.tiles * p.groups;
-  const int64_t want = p.keys ? 4 * kCus : 2 * kCus;        // blocks that fill the chip
-  const int64_t least = p.keys ? 512 : 512;                 // keys worth a block of their own
+  // Blocks that fill the chip, and the keys that are worth a block of their own
+  // (one request of 8192 keys x 8 K/V heads: 15.5 us; with 1024 keys a part
+  // 18.0 us, with 128 20.7 us.  8 of them: 58 us; with twice the blocks 65 us).
+  const int64_t want = 2 * kCus, least = 512;
   const int64_t most = ((int64_t)Skv + least - 1) / least;
   int64_t s = (want + blocks - 1) / blocks;
   if (s > most) s = most;
@@ -621,8 +743,10 @@ svdq_status launch3(const AttnP& p, const Plan& pl, hipStream_t st) {
   else hipLaunchKernelGGL((attention_kernel<DT, DP, PAD, false>), grid, dim3(256), 0, st, p);
   svdq_status s = launched();
   if (s == SVDQ_OK && pl.splits > 1) {
-    const int per = 256 / (DP / 8);
-    hipLaunchKernelGGL((join_kernel<DT, DP>), dim3((unsigned)((pl.rows() + per - 1) / per)), dim3(256), 0, st, p);
+    int across = 1;
+    while (across < 16 && across < pl.splits) across *= 2;
+    const int per = 256 / (DP / 8) / across;
+    hipLaunchKernelGGL((join_kernel<DT, DP>), dim3((unsigned)((pl.rows() + per - 1) / per)), dim3(256), 0, st, p, across);
     s = launched();
   }
   return s;

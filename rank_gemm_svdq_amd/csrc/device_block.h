@@ -63,29 +63,24 @@ __device__ __forceinline__ b4i narrow8(const float* f) {
 // (base wave-uniform, off per lane) land at LDS byte lds + 16 i; inactive
 // lanes copy nothing.  Issued from asm so that the compiler does not serialise
 // it against unrelated LDS reads: completion is waited for explicitly
-// (dma_wait).  M0 is restored before the asm block ends.
+// (dma_wait).  Callers keep base and off ready: the scalar arithmetic of
+// addresses worked out copy by copy costs more than the copies do.
 __device__ __forceinline__ void dma_16(const uint8_t* base, uint32_t off, uint32_t lds) {
-  uint32_t saved;
   asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\t"
-      "global_load_lds_dwordx4 %2, %3\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
+      "s_mov_b32 m0, %0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
-      : "memory");
+      : "memory", "m0");
 }
 // The same with 4 bytes a lane (256 bytes).
 __device__ __forceinline__ void dma_4(const uint8_t* base, uint32_t off, uint32_t lds) {
-  uint32_t saved;
   asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\t"
-      "global_load_lds_dword %2, %3\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
+      "s_mov_b32 m0, %0\n\t"
+      "global_load_lds_dword %1, %2"
+      :
       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
-      : "memory");
+      : "memory", "m0");
 }
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(size_t)(SVDQ_LDS const uint8_t*)p; }

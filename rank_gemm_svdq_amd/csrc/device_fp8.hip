@@ -104,13 +104,17 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
   // token rows past M repeat the last row, lane by lane.
   const int u0 = wave * UNITS;
   const int r8 = lane >> 3, slot = lane & 7;
-  // weights: slot ^ (2 (u % 4) + r8 bit 1); tokens: slot ^ (4 (u % 2) + r8 / 2)
-  const uint32_t voff_w = (uint32_t)r8 * (uint32_t)K + 16u * (slot ^ ((r8 >> 1) & 1));
-  const uint32_t voff_t = (uint32_t)r8 * (uint32_t)K + 16u * (slot ^ (r8 >> 1));
-  const uint32_t voff_e = (uint32_t)min(r8, (M - 1 - m0) & 7) * (uint32_t)K + 16u * (slot ^ (r8 >> 1));
-  const int last_w = (N - n0) / 8 - 1, last_t = (M - 1 - m0) >> 3;
   const uint8_t* wbase = wq + (size_t)n0 * K;
   const uint8_t* tbase = xq + (size_t)m0 * K;
+  uint32_t voff[UNITS];
+#pragma unroll
+  for (int j = 0; j < UNITS; ++j) {
+    const int u = u0 + j, ut = u - T::BN / 8;
+    const bool wside = u < T::BN / 8;
+    const int row = wside ? min(u, (N - n0) / 8 - 1) * 8 + r8 : min(8 * ut + r8, M - 1 - m0);
+    const int f = wside ? 2 * (u & 3) + ((r8 >> 1) & 1) : 4 * (ut & 1) + (r8 >> 1);
+    voff[j] = (uint32_t)row * (uint32_t)K + 16u * (slot ^ f);
+  }
   const uint32_t lds0 = lds_address(lds);
   // scales: lane l the wave's token l (its 16 MT; the others repeat)
   const int m_wave = m0 + 16 * MT * wm;
@@ -119,17 +123,9 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
   auto copy = [&](int v) __attribute__((always_inline)) {   // the v-th of this group's steps
     const int t = v * WK + wk;
     const uint32_t dst = lds0 + (v & 1) * T::STEP + u0 * 1024;
+    const uint8_t *wt = wbase + (size_t)t * 128, *tt = tbase + (size_t)t * 128;
 #pragma unroll
-    for (int j = 0; j < UNITS; ++j) {
-      const int u = u0 + j;
-      if (u < T::BN / 8) {
-        dma_16(wbase + (size_t)min(u, last_w) * 8 * K + (size_t)t * 128, voff_w ^ (32u * (u & 3)), dst + 1024 * j);
-      } else {
-        const int ut = u - T::BN / 8, at = min(ut, last_t);
-        dma_16(tbase + (size_t)at * 8 * K + (size_t)t * 128, (at == last_t ? voff_e : voff_t) ^ (64u * (ut & 1)),
-               dst + 1024 * j);
-      }
-    }
+    for (int j = 0; j < UNITS; ++j) dma_16(u0 + j < T::BN / 8 ? wt : tt, voff[j], dst + 1024 * j);
     dma_4(sbase + (size_t)t * 4, svoff, lds0 + (v & 1) * T::STEP + T::CODES + 256 * wave);
   };
 
