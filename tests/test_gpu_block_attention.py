@@ -216,6 +216,48 @@ def test_long_cache_on_sampled_heads():
                "bf16", f"head {h}", kv_len=n, causal=True)
 
 
+def test_documents_in_a_long_row_on_sampled_queries():
+    """Enough blocks that none shares its keys, and more key tiles than a block looks through beforehand; documents in
+    no order, one of them only at the far end."""
+    Sq, Skv, H, D = 1024, 140000, 64, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    mk = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.float16)
+    q, k, v = mk(1, Sq, H, D), mk(1, Skv, H, D), mk(1, Skv, H, D)
+    rng = np.random.default_rng(9)
+    k_doc = np.full((1, Skv), 99, np.int32)
+    k_doc[0, rng.integers(0, Skv, 3000)] = 1
+    k_doc[0, 500:900] = 2
+    k_doc[0, Skv - 700:] = 3
+    q_doc = np.repeat(np.array([1, 2, 3, 4, 2, 3, 1, 3], np.int32), Sq // 8)[None]
+    o = _gpu(q, k, v, q_doc=q_doc, k_doc=k_doc)
+    for i, h in [(0, 0), (127, 63), (128, 5), (300, 17), (383, 63), (400, 2), (640, 30), (1023, 31)]:
+        _check(o[:, i:i + 1, h:h + 1], values(q[:, i:i + 1, h:h + 1]), values(k[:, :, h:h + 1]), values(v[:, :, h:h + 1]),
+               "fp16", f"query {i} head {h}", q_doc=q_doc[:, i:i + 1], k_doc=k_doc)
+    assert not o[:, 384:512].any()                  # document 4 has no keys
+
+
+@pytest.mark.parametrize("B_,Sq,Hq,Hkv,Skv", [(1, 1, 8, 8, 9000), (3, 5, 6, 1, 5000), (1, 90, 3, 1, 6000)])
+def test_parts_that_see_nothing(B_, Sq, Hq, Hkv, Skv):
+    """Keys split over blocks where the length, the mask and the documents leave whole parts empty."""
+    D = 64
+    (q, qv), (k, kv), (v, vv) = _make(B_, Sq, Skv, Hq, Hkv, D, "bf16", 111)
+    n = [min(Skv, 700 + 10 * b) for b in range(B_)]
+    _check(_gpu(q, k, v, kv_len=n, causal=True), qv, kv, vv, "bf16", "short", kv_len=n, causal=True)
+    k_doc, q_doc = np.zeros((B_, Skv), np.int32), np.ones((B_, Sq), np.int32)
+    k_doc[:, 4321:4330] = 1
+    q_doc[:, Sq // 2:Sq // 2 + 1] = 7               # and one query without any key
+    kw = dict(q_doc=q_doc, k_doc=k_doc)
+    _check(_gpu(q, k, v, **kw), qv, kv, vv, "bf16", "nine keys", **kw)
+
+
+def test_token_strides_out_of_range_are_refused():
+    from tests.test_oracle_block import _attn_args
+    import ctypes as C
+    for change in (dict(k_token=(1 << 25) + 8), dict(v_token=-8), dict(k_token=-8), dict(v_token=(1 << 25) + 8)):
+        assert B.lib().svdq_attention(C.byref(_attn_args(**change)), None, 0, None) == 2
+
+
 @pytest.mark.parametrize("shape", [(1, 1, 5000, 8, 2, 128), (1, 260, 1300, 2, 1, 128), (2, 33, 500, 4, 2, 64)])
 def test_same_bits_again_with_a_used_workspace(shape):
     (q, qv), (k, kv), (v, vv) = _make(*shape, "bf16", 71)

@@ -61,6 +61,20 @@ def test_against_oracle(M, K, N, kind):
     assert torch.equal(Y, _run(xq, xs, wq, ws, kind, bd)), "two runs differ"
 
 
+@pytest.mark.parametrize("M,K,N", [
+    (2300, 384, 2320), (1283, 1152, 4144),          # 128 x 128 tiles, ragged both ways, odd steps
+    (333, 2176, 3088), (200, 1152, 2064),           # 64 x 64, waves in two and four turns
+    (70, 4224, 1040), (20, 65536, 144), (40, 8320, 2048),   # 64 x 32 and 32 x 32; the largest K
+    (1, 65536, 16), (1, 128, 16), (1, 640, 8192), (9, 65536, 32)])
+def test_each_arrangement_at_ragged_sizes(M, K, N):
+    xq, xs, wq, ws = _operands(M, K, N, M + K + N)
+    bd, bv = device(np.random.default_rng(2).standard_normal(N), "bf16")
+    y, mag = O.fp8_linear(xq, xs, wq, ws, bv)
+    Y = _run(xq, xs, wq, ws, "bf16", bd)
+    _check(Y, y, mag, K, "bf16", f"{M}x{K}x{N}")
+    assert torch.equal(Y, _run(xq, xs, wq, ws, "bf16", bd)), "two runs differ"
+
+
 def test_every_row_and_column_is_its_own():
     """One nonzero code in each operand: exactly one output is nonzero, for places all over a ragged shape."""
     M, K, N = 270, 512, 656
