@@ -557,9 +557,10 @@ class _Torch:
         self.values = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 1}   # -> svdq_dtype (int16: bf16 bits)
         self.codes = (torch.float8_e4m3fn, torch.uint8)
         self.bytes = torch.uint8
-        self.current_device = torch.cuda.current_device
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        # the C functions under torch.cuda's, where this torch has them
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 _T = None
@@ -608,17 +609,17 @@ def _rows(t, dev, shape, dtype, what, where):
 
 def _first(t, dims, what, where):
     """(device index, svdq_dtype) of the tensor that the others of a call go by."""
-    T = _tt()
+    T = _T or _tt()
     dev = t.get_device()
-    if dev < 0:
-        raise SvdqError(1, f"{where}: {what} is not in GPU memory")
-    if dev != T.current_device():
-        raise SvdqError(1, f"{where}: {what} is on {t.device}, the current device is cuda:{T.current_device()}")
     code = T.values.get(t.dtype)
-    if code is None:
-        raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected bfloat16, float16 or int16 (bf16 bits)")
-    if t.dim() != dims:
-        raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {dims} dimensions")
+    if code is None or dev < 0 or t.dim() != dims or dev != T.current_device():
+        if dev < 0:
+            raise SvdqError(1, f"{where}: {what} is not in GPU memory")
+        if code is None:
+            raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected bfloat16, float16 or int16 (bf16 bits)")
+        if t.dim() != dims:
+            raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {dims} dimensions")
+        raise SvdqError(1, f"{where}: {what} is on {t.device}, the current device is cuda:{T.current_device()}")
     return dev, code
 
 
@@ -632,18 +633,21 @@ def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=Non
     dev, dt = _first(x, 2, "x", where)
     shape, own = x.shape, x.dtype
     M, K = shape
-    xp, xs = _rows(x, dev, shape, own, "x", where)
-    rp, rs, hp, hs = None, (0,), None, (0,)
-    if residual is not None:
-        rp, rs = _rows(residual, dev, shape, own, "residual", where)
-    if h is not None:
-        hp, hs = _rows(h, dev, shape, own, "h", where)
-    if q.shape != shape:
-        _refuse(q, "q", where, dev, shape, _T.codes, True)
     # the stride of a single row addresses nothing and may be anything
-    st = lib().svdq_add_rmsnorm_quantize(
-        xp, xs[0] if M > 1 else K, rp, rs[0] if M > 1 else K, _whole(weight, dev, (K,), own, "weight", where), eps, M, K,
-        dt, hp, hs[0] if M > 1 else K, _codes(q, dev, "q", where),
+    xp, xs = _rows(x, dev, shape, own, "x", where)
+    rp = hp = None
+    xs = xs[0] if M > 1 else K
+    rs = hs = K
+    if residual is not None:
+        rp, st = _rows(residual, dev, shape, own, "residual", where)
+        rs = st[0] if M > 1 else K
+    if h is not None:
+        hp, st = _rows(h, dev, shape, own, "h", where)
+        hs = st[0] if M > 1 else K
+    if q.dtype not in _T.codes or q.shape != shape or q.get_device() != dev or not q.is_contiguous():
+        _refuse(q, "q", where, dev, shape, _T.codes, True)
+    st = (_lib or lib()).svdq_add_rmsnorm_quantize(
+        xp, xs, rp, rs, _whole(weight, dev, (K,), own, "weight", where), eps, M, K, dt, hp, hs, q.data_ptr(),
         _whole(s, dev, (M, -(-K // FP8_BLOCK)), _T.f32, "s", where),
         _T.stream(dev) if stream is None else stream.cuda_stream)
     if st:
@@ -656,18 +660,19 @@ def fp8_linear(xq, xs, wq, ws, Y, bias=None, stream=None):
     ws [ceil(N / 128), K / 128]; bias [N] has Y's type.  Writes Y [M, N]."""
     where = "svdq_fp8_linear"
     dev, dt = _first(Y, 2, "Y", where)
-    M, N = Y.shape
-    if xq.dim() != 2 or xq.shape[0] != M or wq.shape != (N, xq.shape[1]):
-        raise SvdqError(2, f"{where}: xq {tuple(xq.shape)}, wq {tuple(wq.shape)} and Y ({M}, {N}), expected (M, K), "
+    yshape, xshape = Y.shape, xq.shape
+    M, N = yshape
+    if len(xshape) != 2 or xshape[0] != M or wq.shape != (N, xshape[1]):
+        raise SvdqError(2, f"{where}: xq {tuple(xshape)}, wq {tuple(wq.shape)} and Y ({M}, {N}), expected (M, K), "
                            "(N, K) and (M, N)")
-    K = xq.shape[1]
+    K = xshape[1]
     kb = K // FP8_BLOCK
     f32 = _T.f32
-    st = lib().svdq_fp8_linear(
+    st = (_lib or lib()).svdq_fp8_linear(
         _codes(xq, dev, "xq", where), _whole(xs, dev, (M, kb), f32, "xs", where), _codes(wq, dev, "wq", where),
         _whole(ws, dev, (-(-N // FP8_BLOCK), kb), f32, "ws", where),
         None if bias is None else _whole(bias, dev, (N,), Y.dtype, "bias", where), M, K, N, dt,
-        _whole(Y, dev, (M, N), Y.dtype, "Y", where), _T.stream(dev) if stream is None else stream.cuda_stream)
+        _whole(Y, dev, yshape, Y.dtype, "Y", where), _T.stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SvdqError(st, where)
 
@@ -729,7 +734,7 @@ def rope(plan, positions, x, y, x2=None, y2=None, stream=None):
                         _whole(plan.axis, dev, (plan.pairs,), _T.i32, "the plan's axis", where),
                         xp, x2p, yp, y2p, H, H2, xs[0] * t, x2s[0] * t, xs[1] * h, x2s[1] * h2,
                         ys[0] * t, y2s[0] * t, ys[1] * h, y2s[1] * h2)
-    st = lib().svdq_rope(a, _T.stream(dev) if stream is None else stream.cuda_stream)
+    st = (_lib or lib()).svdq_rope(a, _T.stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SvdqError(st, where)
 
@@ -782,6 +787,6 @@ def attention(q, k, v, o, ws, scale=None, causal=False, softcap=0.0, slopes=None
     if ws is not None:
         wn = ws.numel()
         wp = _whole(ws, dev, ws.shape, _T.bytes, "workspace", where) if wn else None
-    st = lib().svdq_attention(a, wp, wn, _T.stream(dev) if stream is None else stream.cuda_stream)
+    st = (_lib or lib()).svdq_attention(a, wp, wn, _T.stream(dev) if stream is None else stream.cuda_stream)
     if st:
         raise SvdqError(st, where)
