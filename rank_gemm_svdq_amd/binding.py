@@ -9,7 +9,6 @@ no fallback.
 
 import ctypes as C
 import os
-import struct
 
 import numpy as np
 
@@ -536,91 +535,34 @@ def reservoir_select(n_calls, k, seed):
 
 # ------------------------------------------- the operators around the layer
 #
-# Short calls are bound by what happens before the launch, so the checks here
-# are one expression per tensor (the message is put together only on a
-# refusal) and argument structures are packed in one go.
+# Short calls are bound by what happens before the launch, so the tensors of
+# these are checked and marshalled by a small C++ module (csrc/py_block.cpp) over
+# the same C ABI.  Like the library it is built in-tree, and there is no
+# fallback.
 
 FP8_BLOCK = 128                 # SVDQ_FP8_BLOCK
 ROPE_MAX_AXES = 8               # SVDQ_ROPE_MAX_AXES
 ATTENTION_MAX_HEAD_DIM = 128    # SVDQ_ATTENTION_MAX_HEAD_DIM
-_ROPE_PACK = struct.Struct("6i3Q2Q2Q2i8q")
-_ATTENTION_PACK = struct.Struct("8i2f4Q12q5Q")
-assert _ROPE_PACK.size == C.sizeof(RopeArgs) and _ATTENTION_PACK.size == C.sizeof(AttentionArgs)
+BLOCK_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "_block.so")
+_blk = None
 
 
-class _Torch:
-    """What the operators need of torch, looked up on first use."""
-
-    def __init__(self):
-        import torch
-        self.f32, self.i32 = torch.float32, torch.int32
-        self.values = {torch.bfloat16: 0, torch.int16: 0, torch.float16: 1}   # -> svdq_dtype (int16: bf16 bits)
-        self.codes = (torch.float8_e4m3fn, torch.uint8)
-        self.bytes = torch.uint8
-        # the C functions under torch.cuda's, where this torch has them
-        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-_T = None
-
-
-def _tt():
-    global _T
-    if _T is None:
-        _T = _Torch()
-    return _T
-
-
-def _refuse(t, what, where, dev, shape, dtypes, contiguous):
-    """Say what is wrong with a tensor."""
-    if t.get_device() != dev:
-        raise SvdqError(1, f"{where}: {what} is on {t.device}, expected cuda:{dev}")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if shape is not None and t.shape != shape:
-        raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise SvdqError(1, f"{where}: {what} is not contiguous" if contiguous
-                    else f"{where}: the last dimension of {what} is not contiguous")
-
-
-def _whole(t, dev, shape, dtype, what, where):
-    """Address of a contiguous tensor of this device, shape and type."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, what, where, dev, shape, (dtype,), True)
-    return t.data_ptr()
-
-
-def _codes(t, dev, what, where):
-    """Address of a contiguous tensor of E4M3 codes."""
-    if t.dtype not in _T.codes or t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, what, where, dev, None, _T.codes, True)
-    return t.data_ptr()
-
-
-def _rows(t, dev, shape, dtype, what, where):
-    """Address and strides of a tensor whose last dimension is contiguous."""
-    st = t.stride()
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (st[-1] != 1 and shape[-1] > 1):
-        _refuse(t, what, where, dev, shape, (dtype,), False)
-    return t.data_ptr(), st
-
-
-def _first(t, dims, what, where):
-    """(device index, svdq_dtype) of the tensor that the others of a call go by."""
-    T = _T or _tt()
-    dev = t.get_device()
-    code = T.values.get(t.dtype)
-    if code is None or dev < 0 or t.dim() != dims or dev != T.current_device():
-        if dev < 0:
-            raise SvdqError(1, f"{where}: {what} is not in GPU memory")
-        if code is None:
-            raise SvdqError(1, f"{where}: {what} has dtype {t.dtype}, expected bfloat16, float16 or int16 (bf16 bits)")
-        if t.dim() != dims:
-            raise SvdqError(2, f"{where}: {what} has shape {tuple(t.shape)}, expected {dims} dimensions")
-        raise SvdqError(1, f"{where}: {what} is on {t.device}, the current device is cuda:{T.current_device()}")
-    return dev, code
+def _block():
+    """Load the marshalling module (once) and bind it to the library."""
+    global _blk
+    if _blk is None:
+        import importlib.util
+        _torch()                # its shared libraries first
+        if not os.path.exists(BLOCK_PATH):
+            raise RuntimeError(f"_block.so not built ({BLOCK_PATH}); run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("_block", BLOCK_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(SvdqError, *(C.cast(f, C.c_void_p).value
+                            for f in (L.svdq_add_rmsnorm_quantize, L.svdq_fp8_linear, L.svdq_rope, L.svdq_attention)))
+        _blk = m
+    return _blk
 
 
 def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=None):
@@ -629,52 +571,14 @@ def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=Non
     [M, K] (rows may be strided; h may be x or residual); weight [K];
     q [M, K] float8_e4m3fn or uint8; s [M, ceil(K / 128)] float32.  Writes q, s
     and, if given, h."""
-    where = "svdq_add_rmsnorm_quantize"
-    dev, dt = _first(x, 2, "x", where)
-    shape, own = x.shape, x.dtype
-    M, K = shape
-    # the stride of a single row addresses nothing and may be anything
-    xp, xs = _rows(x, dev, shape, own, "x", where)
-    rp = hp = None
-    xs = xs[0] if M > 1 else K
-    rs = hs = K
-    if residual is not None:
-        rp, st = _rows(residual, dev, shape, own, "residual", where)
-        rs = st[0] if M > 1 else K
-    if h is not None:
-        hp, st = _rows(h, dev, shape, own, "h", where)
-        hs = st[0] if M > 1 else K
-    if q.dtype not in _T.codes or q.shape != shape or q.get_device() != dev or not q.is_contiguous():
-        _refuse(q, "q", where, dev, shape, _T.codes, True)
-    st = (_lib or lib()).svdq_add_rmsnorm_quantize(
-        xp, xs, rp, rs, _whole(weight, dev, (K,), own, "weight", where), eps, M, K, dt, hp, hs, q.data_ptr(),
-        _whole(s, dev, (M, -(-K // FP8_BLOCK)), _T.f32, "s", where),
-        _T.stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise SvdqError(st, where)
+    (_blk or _block()).add_rmsnorm_quantize(x, weight, eps, q, s, residual, h, stream)
 
 
 def fp8_linear(xq, xs, wq, ws, Y, bias=None, stream=None):
     """svdq_fp8_linear: Y = (xq xs) (wq ws)^T + bias with E4M3 codes xq [M, K],
     wq [N, K] (float8_e4m3fn or uint8) and fp32 scales xs [M, K / 128],
     ws [ceil(N / 128), K / 128]; bias [N] has Y's type.  Writes Y [M, N]."""
-    where = "svdq_fp8_linear"
-    dev, dt = _first(Y, 2, "Y", where)
-    yshape, xshape = Y.shape, xq.shape
-    M, N = yshape
-    if len(xshape) != 2 or xshape[0] != M or wq.shape != (N, xshape[1]):
-        raise SvdqError(2, f"{where}: xq {tuple(xshape)}, wq {tuple(wq.shape)} and Y ({M}, {N}), expected (M, K), "
-                           "(N, K) and (M, N)")
-    K = xshape[1]
-    kb = K // FP8_BLOCK
-    f32 = _T.f32
-    st = (_lib or lib()).svdq_fp8_linear(
-        _codes(xq, dev, "xq", where), _whole(xs, dev, (M, kb), f32, "xs", where), _codes(wq, dev, "wq", where),
-        _whole(ws, dev, (-(-N // FP8_BLOCK), kb), f32, "ws", where),
-        None if bias is None else _whole(bias, dev, (N,), Y.dtype, "bias", where), M, K, N, dt,
-        _whole(Y, dev, yshape, Y.dtype, "Y", where), _T.stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise SvdqError(st, where)
+    (_blk or _block()).fp8_linear(xq, xs, wq, ws, Y, bias, stream)
 
 
 def rope_frequencies(dims, theta=10000.0, shared=False):
@@ -708,35 +612,8 @@ def rope(plan, positions, x, y, x2=None, y2=None, stream=None):
     beside the queries) by the angles of positions [M, axes] (int32).  x, y
     [M, heads, head_dim], x2, y2 [M, heads2, head_dim], any token and head
     strides that are multiples of 8 elements; y may be x."""
-    where = "svdq_rope"
-    dev, dt = _first(x, 3, "x", where)
-    shape, own = x.shape, x.dtype
-    M, H, D = shape
-    xp, xs = _rows(x, dev, shape, own, "x", where)
-    yp, ys = _rows(y, dev, shape, own, "y", where)
-    x2p = y2p = H2 = 0
-    x2s = y2s = (0, 0)
-    if x2 is not None and y2 is not None:
-        shape2 = x2.shape
-        if len(shape2) != 3 or shape2[0] != M or shape2[2] != D:
-            raise SvdqError(2, f"{where}: x2 has shape {tuple(shape2)}, expected ({M}, heads, {D})")
-        H2 = shape2[1]
-        x2p, x2s = _rows(x2, dev, shape2, own, "x2", where)
-        y2p, y2s = _rows(y2, dev, shape2, own, "y2", where)
-    elif x2 is not None or y2 is not None:
-        raise SvdqError(1, f"{where}: x2 and y2 go together")
-    # strides of dimensions with one place address nothing: 0
-    t = M > 1
-    h, h2 = H > 1, H2 > 1
-    a = _ROPE_PACK.pack(M, plan.axes, plan.pairs, D, plan.interleaved, dt,
-                        _whole(positions, dev, (M, plan.axes), _T.i32, "positions", where),
-                        _whole(plan.turns, dev, (plan.pairs, 2), _T.f32, "the plan's turns", where),
-                        _whole(plan.axis, dev, (plan.pairs,), _T.i32, "the plan's axis", where),
-                        xp, x2p, yp, y2p, H, H2, xs[0] * t, x2s[0] * t, xs[1] * h, x2s[1] * h2,
-                        ys[0] * t, y2s[0] * t, ys[1] * h, y2s[1] * h2)
-    st = (_lib or lib()).svdq_rope(a, _T.stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise SvdqError(st, where)
+    (_blk or _block()).rope(plan.turns, plan.axis, plan.axes, plan.pairs, plan.interleaved, positions, x, y, x2, y2,
+                            stream)
 
 
 def attention_workspace_bytes(B, Sq, Skv, Hq, Hkv, D):
@@ -757,36 +634,4 @@ def attention(q, k, v, o, ws, scale=None, causal=False, softcap=0.0, slopes=None
     dimension contiguous); ws from attention_workspace().  scale: D ** -0.5
     if None.  slopes [Hq] float32; kv_len, prefix [B], q_doc [B, Sq], k_doc
     [B, Skv] int32.  The queries are the last Sq of the kv_len keys' positions."""
-    where = "svdq_attention"
-    dev, dt = _first(q, 4, "q", where)
-    shape, kshape, own = q.shape, k.shape, q.dtype
-    B, Sq, Hq, D = shape
-    if len(kshape) != 4 or kshape[0] != B or kshape[3] != D:
-        raise SvdqError(2, f"{where}: q {tuple(shape)} and k {tuple(kshape)}, expected (B, Sq, Hq, D) and "
-                           "(B, Skv, Hkv, D)")
-    Skv, Hkv = kshape[1], kshape[2]
-    qp, qs = _rows(q, dev, shape, own, "q", where)
-    kp, ks = _rows(k, dev, kshape, own, "k", where)
-    vp, vs = _rows(v, dev, kshape, own, "v", where)
-    op, os_ = _rows(o, dev, shape, own, "o", where)
-    i32 = _T.i32
-    if (q_doc is None) != (k_doc is None):
-        raise SvdqError(1, f"{where}: q_doc and k_doc go together")
-    # strides of dimensions with one place address nothing: 0
-    b, i, h, j, g = B > 1, Sq > 1, Hq > 1, Skv > 1, Hkv > 1
-    a = _ATTENTION_PACK.pack(
-        B, Sq, Skv, Hq, Hkv, D, dt, bool(causal), D ** -0.5 if scale is None else scale, softcap, qp, kp, vp, op,
-        qs[0] * b, qs[1] * i, qs[2] * h, ks[0] * b, ks[1] * j, ks[2] * g, vs[0] * b, vs[1] * j, vs[2] * g,
-        os_[0] * b, os_[1] * i, os_[2] * h,
-        0 if slopes is None else _whole(slopes, dev, (Hq,), _T.f32, "slopes", where),
-        0 if kv_len is None else _whole(kv_len, dev, (B,), i32, "kv_len", where),
-        0 if prefix is None else _whole(prefix, dev, (B,), i32, "prefix", where),
-        0 if q_doc is None else _whole(q_doc, dev, (B, Sq), i32, "q_doc", where),
-        0 if k_doc is None else _whole(k_doc, dev, (B, Skv), i32, "k_doc", where))
-    wp, wn = None, 0
-    if ws is not None:
-        wn = ws.numel()
-        wp = _whole(ws, dev, ws.shape, _T.bytes, "workspace", where) if wn else None
-    st = (_lib or lib()).svdq_attention(a, wp, wn, _T.stream(dev) if stream is None else stream.cuda_stream)
-    if st:
-        raise SvdqError(st, where)
+    (_blk or _block()).attention(q, k, v, o, ws, scale, causal, softcap, slopes, kv_len, prefix, q_doc, k_doc, stream)

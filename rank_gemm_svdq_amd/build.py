@@ -1,4 +1,5 @@
-"""Build the C-ABI shared library in-tree (rank_gemm_svdq_amd/lib/libsvdq.so).
+"""Build the C-ABI shared library in-tree (rank_gemm_svdq_amd/lib/libsvdq.so)
+and the Python module that marshals the block operators' tensors (lib/_block.so).
 
 Host sources are compiled with g++ (x86-64-v3, no fp contraction in the
 packers), device sources with hipcc for gfx950; hipcc links the library.
@@ -31,6 +32,33 @@ UNITS = [
     ("device_search.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_probe.hip", [HIPCC] + DEVICE_FLAGS),
 ]
+
+# The marshalling module of the block operators: a CPython extension against
+# torch's headers, without the library's code (it is handed the addresses).
+EXT = os.path.join(LIBDIR, "_block.so")
+
+
+def _ext_command(out):
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], "/opt/rocm/include"]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+            + [f"-I{d}" for d in inc] + [os.path.join(CSRC, "py_block.cpp"), "-o", out]
+            + [f"-L{os.path.join(t, 'lib')}", f"-Wl,-rpath,{os.path.join(t, 'lib')}",
+               "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"])
+
+
+def build_ext():
+    """Compile the marshalling module in-tree (lib/_block.so)."""
+    os.makedirs(LIBDIR, exist_ok=True)
+    tmp = EXT + ".tmp"
+    _run(_ext_command(tmp))
+    os.replace(tmp, EXT)
+    return EXT
 
 
 def _run(cmd):
@@ -86,6 +114,7 @@ def build(verbose=False, sanitize=False, reuse_device_objects=False):
              ["-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-lpthread"])
     else:
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs + ["-lpthread"])
+        build_ext()
     os.replace(tmp, lib)
     return lib
 
