@@ -64,10 +64,12 @@ __device__ __forceinline__ b4i narrow8(const float* f) {
 // lanes copy nothing.  Issued from asm so that the compiler does not serialise
 // it against unrelated LDS reads: completion is waited for explicitly
 // (dma_wait).  Callers keep base and off ready: the scalar arithmetic of
-// addresses worked out copy by copy costs more than the copies do.
+// addresses worked out copy by copy costs more than the copies do.  The load
+// needs one wait state after the write of M0.
 __device__ __forceinline__ void dma_16(const uint8_t* base, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
@@ -77,6 +79,7 @@ __device__ __forceinline__ void dma_16(const uint8_t* base, uint32_t off, uint32
 __device__ __forceinline__ void dma_4(const uint8_t* base, uint32_t off, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
       "global_load_lds_dword %1, %2"
       :
       : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base)
