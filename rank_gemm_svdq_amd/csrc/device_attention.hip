@@ -722,14 +722,34 @@ Plan plan_of(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_
   p.keys = p.R <= 32;
   p.tiles = p.keys ? 1 : (p.R + 127) / 128;
   const int64_t blocks = (int64_t)p.tiles * p.groups;
-  // Blocks that fill the chip, and the keys that are worth a block of their own
-  // (one request of 8192 keys x 8 K/V heads: 15.5 us; with 1024 keys a part
-  // 18.0 us, with 128 20.7 us.  8 of them: 58 us; with twice the blocks 65 us).
-  const int64_t want = 2 * kCus, least = 512;
-  const int64_t most = ((int64_t)Skv + least - 1) / least;
-  int64_t s = (want + blocks - 1) / blocks;
-  if (s > most) s = most;
-  if (s > 64) s = 64;
+  // Blocks that the chip holds, and the keys that are worth a block of their own.
+  const int64_t fill = 2 * kCus, least = 512;
+  int64_t most = ((int64_t)Skv + least - 1) / least;
+  if (most > 64) most = 64;
+  int64_t s = 1;
+  if (p.keys) {
+    // as many as fill the chip (one request of 8192 keys x 8 K/V heads: 15.5
+    // us; with 1024 keys a part 18.0 us, with 128 20.7 us.  8 of them: 58 us;
+    // with twice the blocks 65 us)
+    s = (fill + blocks - 1) / blocks;
+    if (s > most) s = most;
+  } else if (blocks < fill) {
+    // the least time, in half tiles of 64 keys: rounds of blocks, each with its
+    // share of the keys and about 6 tiles' worth of start and end, and the join.
+    // (Against as many parts as fill the chip: 2 x 700 queries of 16 heads on
+    // 3001 keys, 68 for 73 us; 1024 of 24 on 4096, 78 for 95; 2500 of 16 on as
+    // many, 93 for 87.)
+    const int64_t t = ((int64_t)Skv + 63) / 64;
+    int64_t best = 0;
+    for (int64_t k = 1; k <= most; ++k) {
+      const int64_t rounds = (blocks * k + fill - 1) / fill;
+      const int64_t cost = 2 * rounds * ((t + k - 1) / k + 6) + (k > 1 ? 8 + k : 0);
+      if (k == 1 || cost < best) {
+        best = cost;
+        s = k;
+      }
+    }
+  }
   p.splits = s < 1 ? 1 : (int)s;
   (void)D;
   return p;
