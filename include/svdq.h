@@ -409,6 +409,18 @@ svdq_status svdq_fp8_linear(const uint8_t* xq, const float* xs, const uint8_t* w
                             const uint16_t* bias, int32_t M, int32_t K, int32_t N, int32_t dtype, uint16_t* Y,
                             void* stream);
 
+/* The same product with memory in which blocks leave partial sums (fp32, added
+ * in a fixed order), so that they can share a long K where the output has few
+ * tiles.  svdq_fp8_linear_workspace_bytes: what a call of this shape uses, at
+ * most 32 MiB, and 0 where sharing does not pay; then workspace may be NULL
+ * and the call is svdq_fp8_linear.  The contents before the call do not
+ * matter; calls on one stream may use the same memory.
+ * Errors: as svdq_fp8_linear (workspace: 16 bytes), WORKSPACE. */
+size_t svdq_fp8_linear_workspace_bytes(int32_t M, int32_t K, int32_t N);
+svdq_status svdq_fp8_linear_shared(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                                   const uint16_t* bias, int32_t M, int32_t K, int32_t N, int32_t dtype, uint16_t* Y,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 #define SVDQ_ROPE_MAX_AXES 8
 
 /* Frequencies of rotary positions with several axes.  Axis a owns dims[a] / 2

@@ -19,7 +19,7 @@ __all__ = [
     "quantize_lora_down", "gemm_lora_up", "linear_forward", "linear_forward_unfused", "linear_forward_noalloc",
     "NOALLOC_MAX_WORKSPACE", "fmt_code", "LIB_PATH",
     "ABI_VERSION", "mfma_rate_probe", "reservoir_select", "smooth_candidates", "search_workspace_bytes", "smooth_search", "SearchOpts", "SearchResult",
-    "add_rmsnorm_quantize", "fp8_linear", "rope_frequencies", "RopePlan", "rope", "attention",
+    "add_rmsnorm_quantize", "fp8_linear", "fp8_linear_workspace_bytes", "rope_frequencies", "RopePlan", "rope", "attention",
     "attention_workspace", "attention_workspace_bytes", "FP8_BLOCK", "ROPE_MAX_AXES", "ATTENTION_MAX_HEAD_DIM",
 ]
 
@@ -169,6 +169,9 @@ def lib():
     L.svdq_add_rmsnorm_quantize.argtypes = [vp, C.c_int64, vp, C.c_int64, vp, C.c_float, i32, i32, i32, vp, C.c_int64,
                                             vp, vp, vp]
     L.svdq_fp8_linear.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
+    L.svdq_fp8_linear_workspace_bytes.restype = sz
+    L.svdq_fp8_linear_workspace_bytes.argtypes = [i32] * 3
+    L.svdq_fp8_linear_shared.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]
     L.svdq_rope_frequencies.argtypes = [i32, vp, C.c_double, i32, vp, vp]
     L.svdq_rope.argtypes = [vp, vp]             # svdq_rope_args
     L.svdq_attention_workspace_bytes.restype = sz
@@ -178,8 +181,8 @@ def lib():
                  "svdq_pack_host", "svdq_prepare", "svdq_attach_lora", "svdq_kernel_layout",
                  "svdq_unpack_activations", "svdq_quantize_lora_down", "svdq_gemm_lora_up",
                  "svdq_linear_forward", "svdq_linear_forward_unfused", "svdq_linear_forward_noalloc",
-                 "svdq_smooth_search", "svdq_add_rmsnorm_quantize", "svdq_fp8_linear", "svdq_rope_frequencies",
-                 "svdq_rope", "svdq_attention"):
+                 "svdq_smooth_search", "svdq_add_rmsnorm_quantize", "svdq_fp8_linear",
+                 "svdq_fp8_linear_shared", "svdq_rope_frequencies", "svdq_rope", "svdq_attention"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -560,7 +563,8 @@ def _block():
         spec.loader.exec_module(m)
         L = lib()
         m.bind(SvdqError, *(C.cast(f, C.c_void_p).value
-                            for f in (L.svdq_add_rmsnorm_quantize, L.svdq_fp8_linear, L.svdq_rope, L.svdq_attention)))
+                            for f in (L.svdq_add_rmsnorm_quantize, L.svdq_fp8_linear_shared,
+                                      L.svdq_fp8_linear_workspace_bytes, L.svdq_rope, L.svdq_attention)))
         _blk = m
     return _blk
 
@@ -574,11 +578,17 @@ def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=Non
     (_blk or _block()).add_rmsnorm_quantize(x, weight, eps, q, s, residual, h, stream)
 
 
-def fp8_linear(xq, xs, wq, ws, Y, bias=None, stream=None):
-    """svdq_fp8_linear: Y = (xq xs) (wq ws)^T + bias with E4M3 codes xq [M, K],
+def fp8_linear_workspace_bytes(M, K, N):
+    return lib().svdq_fp8_linear_workspace_bytes(M, K, N)
+
+
+def fp8_linear(xq, xs, wq, ws, Y, bias=None, workspace=None, stream=None):
+    """svdq_fp8_linear_shared: Y = (xq xs) (wq ws)^T + bias with E4M3 codes xq [M, K],
     wq [N, K] (float8_e4m3fn or uint8) and fp32 scales xs [M, K / 128],
-    ws [ceil(N / 128), K / 128]; bias [N] has Y's type.  Writes Y [M, N]."""
-    (_blk or _block()).fp8_linear(xq, xs, wq, ws, Y, bias, stream)
+    ws [ceil(N / 128), K / 128]; bias [N] has Y's type.  Writes Y [M, N].
+    workspace: uint8, fp8_linear_workspace_bytes() long; without one a call
+    that needs it (few tiles, long K) takes it from torch's allocator."""
+    (_blk or _block()).fp8_linear(xq, xs, wq, ws, Y, bias, workspace, stream)
 
 
 def rope_frequencies(dims, theta=10000.0, shared=False):

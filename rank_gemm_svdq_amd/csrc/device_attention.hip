@@ -51,7 +51,6 @@ namespace svdq {
 namespace {
 
 constexpr int kSeen = 2048;  // tiles of a block looked through for their documents
-constexpr int kCus = 256;   // compute units of the chip, for the host-side choice of splits
 
 struct Part {               // how the keys are split over blocks
   int32_t splits;

@@ -96,6 +96,8 @@ __device__ __forceinline__ int xcd_order(int b, int total) {
   return x * q + min(x, r) + (b >> 3);
 }
 
+constexpr int kCus = 256;   // compute units of the chip, for the choice of variants on the host
+
 inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool on4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 inline bool is_dtype(int32_t d) { return d == SVDQ_BF16 || d == SVDQ_FP16; }

@@ -73,11 +73,15 @@ struct Tile {
   static constexpr int LDS = 2 * WK * STEP > JOIN ? 2 * WK * STEP : JOIN;
 };
 
-template <int DT, int NT, int MT, int WN, int WM, int WK>
+// Long k and few tiles: a 128 x 128 tile moves half the bytes per product of a
+// 64 x 64 one, but 333 x 12288 -> 3072 has 72 of them.  SPLIT: `parts` blocks share a tile's steps and leave their sums in `sums`, as
+// [part][tile][wave][nt][mt][lane], for fp8_join_kernel.
+template <int DT, int NT, int MT, int WN, int WM, int WK, bool SPLIT>
 __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, const uint16_t* __restrict__ bias, int M, int K, int N, uint16_t* __restrict__ Y,
-    int tiles_m, int tiles_n) {
+    int tiles_m, int tiles_n, int parts, b4f* __restrict__ sums) {
+  static_assert(!SPLIT || WK == 1, "blocks or groups share the steps");
   using T = Tile<NT, MT, WN, WM, WK>;
   constexpr int UNITS = T::UNITS;
   static_assert(MT <= 4 && NT % 2 == 0, "64 token scales per wave, pairs of weight tiles");
@@ -91,12 +95,20 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
   const int l16 = lane & 15, g = lane >> 4;
   // work ids run through groups of 8 token tiles, out-feature tile slower: the
   // blocks that an XCD holds at a time share their operand panels in its L2
-  const int id = xcd_order(blockIdx.x, tiles_m * tiles_n);
+  int id = xcd_order(blockIdx.x, tiles_m * tiles_n * (SPLIT ? parts : 1)), part = 0;
+  const int place = id;
+  if constexpr (SPLIT) {
+    part = id / (tiles_m * tiles_n);
+    id -= part * (tiles_m * tiles_n);
+  }
   const int span = 8 * tiles_n, grp = id / span, in = id % span;
   const int high = min(8, tiles_m - 8 * grp);
   const int m0 = (8 * grp + in % high) * T::BM, n0 = (in / high) * T::BN;
   const int steps = K >> 7;
-  const int mine = (steps - wk + WK - 1) / WK, turns = (steps + WK - 1) / WK;   // steps wk, wk + WK, ...
+  // steps wk, wk + WK, ..., or the part's
+  const int first = SPLIT ? part * steps / parts : wk;
+  const int mine = SPLIT ? (part + 1) * steps / parts - first : (steps - wk + WK - 1) / WK;
+  const int turns = SPLIT ? mine : (steps + WK - 1) / WK;
   uint8_t* lds = lds_all + wk * 2 * T::STEP;
 
   // ---- copies: units of 8 rows, weights first.  N % 16 == 0, so a unit of
@@ -121,7 +133,7 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
   const uint8_t* sbase = reinterpret_cast<const uint8_t*>(xs + (size_t)min(m_wave, M - 1) * steps);
   const uint32_t svoff = (uint32_t)max(min(lane & (16 * MT - 1), M - 1 - m_wave), 0) * (uint32_t)steps * 4u;
   auto copy = [&](int v) __attribute__((always_inline)) {   // the v-th of this group's steps
-    const int t = v * WK + wk;
+    const int t = v * WK + first;
     const uint32_t dst = lds0 + (v & 1) * T::STEP + u0 * 1024;
     const uint8_t *wt = wbase + (size_t)t * 128, *tt = tbase + (size_t)t * 128;
 #pragma unroll
@@ -156,7 +168,7 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
     __syncthreads();
     if (v + 1 < mine) copy(v + 1);
     if (WK > 1 && v >= mine) break;                         // the last turn of a group with one step less
-    const float sw = swl[v * WK + wk];
+    const float sw = swl[v * WK + first];
     const uint8_t* buf = lds + (v & 1) * T::STEP;
     const float* sx = reinterpret_cast<const float*>(buf + T::CODES + 256 * wave);
     b4i blo, bhi;
@@ -231,6 +243,15 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
         for (int mt = 0; mt < MT; ++mt) acc[nt][mt] += j[(((k * T::WAVES + wave) * NT + nt) * MT + mt) * 64 + lane];
   }
 
+  if constexpr (SPLIT) {
+    b4f* out = sums + ((size_t)place * T::WAVES + wave) * NT * MT * 64 + lane;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) out[(nt * MT + mt) * 64] = acc[nt][mt];
+    return;
+  }
+
 #pragma unroll
   for (int pr = 0; pr < NT / 2; ++pr) {
     const int n = n0 + 16 * NT * wn + 32 * pr + 8 * g;
@@ -252,6 +273,41 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
       *reinterpret_cast<b4i*>(Y + (size_t)m * N + n) = narrow8<DT>(v);
     }
   }
+}
+
+// Adds the parts of a tile in their order.  A block takes one (pair of weight
+// tiles, token tile) of all waves of a tile; lanes hold what they held there.
+template <int DT, int NT, int MT, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM) void fp8_join_kernel(const b4f* __restrict__ sums,
+                                                                const uint16_t* __restrict__ bias, int M, int N,
+                                                                uint16_t* __restrict__ Y, int tiles_m, int tiles_n,
+                                                                int parts) {
+  using T = Tile<NT, MT, WN, WM, 1>;
+  constexpr int PIECES = NT / 2 * MT;
+  const int id = blockIdx.x / PIECES, piece = blockIdx.x % PIECES, pr = piece / MT, mt = piece % MT;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, wm = wave % WM, wn = wave / WM;
+  const int span = 8 * tiles_n, grp = id / span, in = id % span;
+  const int high = min(8, tiles_m - 8 * grp);
+  const int m = (8 * grp + in % high) * T::BM + 16 * MT * wm + 16 * mt + (lane & 15);
+  const int n = (in / high) * T::BN + 16 * NT * wn + 32 * pr + 8 * (lane >> 4);
+  if (m >= M || n >= N) return;
+  const b4f* at = sums + (((size_t)id * T::WAVES + wave) * NT * MT + (2 * pr) * MT + mt) * 64 + lane;
+  const size_t next = (size_t)tiles_m * tiles_n * T::WAVES * NT * MT * 64;
+  b4f lo = at[0], hi = at[MT * 64];
+#pragma unroll 4
+  for (int p = 1; p < parts; ++p) {
+    at += next;
+    lo += at[0];
+    hi += at[MT * 64];
+  }
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = lo[i];
+    v[4 + i] = hi[i];
+  }
+  add_bias8<DT>(bias, n, v);
+  *reinterpret_cast<b4i*>(Y + (size_t)m * N + n) = narrow8<DT>(v);
 }
 
 // ------------------------------------------------------------ few tokens
@@ -368,6 +424,40 @@ __global__ __launch_bounds__(256) void fp8_row_kernel(const uint8_t* __restrict_
   }
 }
 
+// In how many parts the steps of a 128 x 128 tile are taken by blocks of their
+// own, given memory for their sums: as many as the chip holds (two blocks a
+// compute unit), where k is long enough to pay for the sums' way through
+// memory and the second launch.  Measured, us (without -> with):
+//   K      100 x 3072    200 x 3072    333 x 3072    512 x 3072    512 x 4096
+//   6144   15 -> 19      20 -> 23      31 -> 26      32 -> 32      35 -> 36
+//   8192   19 -> 19      25 -> 25      39 -> 31      40 -> 36      44 -> 43
+//   12288  27 -> 22      35 -> 30      59 -> 39      61 -> 47      68 -> 57
+//   16384  31 -> 25      44 -> 35      74 -> 46      76 -> 58      90 -> 76
+// (M x N in the head.)  16 tiles lose at any K (100 x 16384 -> 2048 20 -> 25),
+// and so do few tokens (64 x 12288 -> 3072 17.5 -> 21.7).
+int64_t fp8_tiles(int M, int N) { return (int64_t)((M + 127) / 128) * ((N + 127) / 128); }
+int fp8_parts(int M, int K, int N) {
+  const int64_t tiles = fp8_tiles(M, N), steps = K / 128;
+  if (M <= 64 || steps < 64 || tiles < 24 || tiles > kCus || 2 * tiles + 3 * steps < 336) return 1;
+  return (int)(2 * kCus / tiles);                            // at most 21
+}
+
+template <int DT>
+svdq_status launch_split(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const uint16_t* bias,
+                         int M, int K, int N, uint16_t* Y, b4f* sums, hipStream_t st) {
+  const int tm = (M + 127) / 128, tn = (N + 127) / 128, parts = fp8_parts(M, K, N);
+  hipLaunchKernelGGL((fp8_tile_kernel<DT, 4, 4, 2, 2, 1, true>), dim3(tm * tn * parts), dim3(256), 0, st, xq, xs, wq,
+                     ws, nullptr, M, K, N, nullptr, tm, tn, parts, sums);
+  hipLaunchKernelGGL((fp8_join_kernel<DT, 4, 4, 2, 2>), dim3(tm * tn * 8), dim3(256), 0, st, sums, bias, M, N, Y, tm,
+                     tn, parts);
+  return launched();
+}
+
+bool fp8_sizes(int32_t M, int32_t K, int32_t N) {
+  return valid_kn(K, N) && M >= 1 && M <= (1 << 20) && (int64_t)M * K <= (int64_t)1 << 32 &&
+         (int64_t)N * K <= (int64_t)1 << 32;
+}
+
 // The variant of a call, by its sizes.  Tiles are taken as large as the chip
 // can still be filled with (256 compute units), and where they are few, waves
 // take the steps of k in turn.  Measured, us (tile side or sides, groups):
@@ -401,8 +491,8 @@ svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, co
                   WM = decltype(wm)::value, WK = decltype(wk)::value;
     using T = Tile<NT, MT, WN, WM, WK>;
     const int tm = (M + T::BM - 1) / T::BM, tn = (N + T::BN - 1) / T::BN;
-    hipLaunchKernelGGL((fp8_tile_kernel<DT, NT, MT, WN, WM, WK>), dim3(tm * tn), dim3(64 * T::WAVES * WK), 0, st,
-                       xq, xs, wq, ws, bias, M, K, N, Y, tm, tn);
+    hipLaunchKernelGGL((fp8_tile_kernel<DT, NT, MT, WN, WM, WK, false>), dim3(tm * tn), dim3(64 * T::WAVES * WK), 0, st,
+                       xq, xs, wq, ws, bias, M, K, N, Y, tm, tn, 1, nullptr);
   };
   if (M == 1) {
     if (N >= 6144) row(I2{});   // 3072 -> 9216: 7.3 us against 7.7 with one row; 12288 -> 3072: 9.1 against 8.4
@@ -429,17 +519,50 @@ svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, co
 
 using namespace svdq;
 
+namespace {
+
+svdq_status fp8_check(const void* xq, const void* xs, const void* wq, const void* ws, const void* bias, int32_t M,
+                      int32_t K, int32_t N, int32_t dtype, const void* Y) {
+  if (!xq || !xs || !wq || !ws || !Y) return SVDQ_ERR_ARG;
+  if (!is_dtype(dtype)) return SVDQ_ERR_UNSUPPORTED;
+  if (!fp8_sizes(M, K, N)) return SVDQ_ERR_SHAPE;
+  if (!on16(xq) || !on16(wq) || !on16(bias) || !on16(Y) || !on4(xs) || !on4(ws)) return SVDQ_ERR_ALIGN;
+  return SVDQ_OK;
+}
+
+}  // namespace
+
 extern "C" svdq_status svdq_fp8_linear(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
                                        const uint16_t* bias, int32_t M, int32_t K, int32_t N, int32_t dtype,
                                        uint16_t* Y, void* stream) {
-  if (!xq || !xs || !wq || !ws || !Y) return SVDQ_ERR_ARG;
-  if (!is_dtype(dtype)) return SVDQ_ERR_UNSUPPORTED;
-  if (!valid_kn(K, N) || M < 1 || M > (1 << 20)) return SVDQ_ERR_SHAPE;
-  if ((int64_t)M * K > (int64_t)1 << 32 || (int64_t)N * K > (int64_t)1 << 32) return SVDQ_ERR_SHAPE;
-  if (!on16(xq) || !on16(wq) || !on16(bias) || !on16(Y) || !on4(xs) || !on4(ws)) return SVDQ_ERR_ALIGN;
-  const svdq_status ok = device_ok();
+  svdq_status ok = fp8_check(xq, xs, wq, ws, bias, M, K, N, dtype, Y);
+  if (ok == SVDQ_OK) ok = device_ok();
   if (ok != SVDQ_OK) return ok;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return dtype == SVDQ_BF16 ? launch_fp8<SVDQ_BF16>(xq, xs, wq, ws, bias, M, K, N, Y, st)
                             : launch_fp8<SVDQ_FP16>(xq, xs, wq, ws, bias, M, K, N, Y, st);
+}
+
+extern "C" size_t svdq_fp8_linear_workspace_bytes(int32_t M, int32_t K, int32_t N) {
+  if (!fp8_sizes(M, K, N)) return 0;
+  const int parts = fp8_parts(M, K, N);
+  return parts > 1 ? (size_t)parts * fp8_tiles(M, N) * 128 * 128 * sizeof(float) : 0;
+}
+
+extern "C" svdq_status svdq_fp8_linear_shared(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,
+                                              const uint16_t* bias, int32_t M, int32_t K, int32_t N, int32_t dtype,
+                                              uint16_t* Y, void* workspace, size_t workspace_bytes, void* stream) {
+  const size_t need = svdq_fp8_linear_workspace_bytes(M, K, N);
+  if (need == 0) return svdq_fp8_linear(xq, xs, wq, ws, bias, M, K, N, dtype, Y, stream);
+  svdq_status ok = fp8_check(xq, xs, wq, ws, bias, M, K, N, dtype, Y);
+  if (ok != SVDQ_OK) return ok;
+  if (!workspace) return SVDQ_ERR_ARG;
+  if (workspace_bytes < need) return SVDQ_ERR_WORKSPACE;
+  if (!on16(workspace)) return SVDQ_ERR_ALIGN;
+  ok = device_ok();
+  if (ok != SVDQ_OK) return ok;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  b4f* sums = static_cast<b4f*>(workspace);
+  return dtype == SVDQ_BF16 ? launch_split<SVDQ_BF16>(xq, xs, wq, ws, bias, M, K, N, Y, sums, st)
+                            : launch_split<SVDQ_FP16>(xq, xs, wq, ws, bias, M, K, N, Y, sums, st);
 }

@@ -9,6 +9,7 @@
 // works on whichever build of the library the package has loaded.
 
 #include <ATen/core/Tensor.h>
+#include <c10/hip/HIPCachingAllocator.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -24,7 +25,8 @@ namespace {
 
 PyObject* g_error = nullptr;                       // SvdqError(status, text)
 decltype(&svdq_add_rmsnorm_quantize) g_norm = nullptr;
-decltype(&svdq_fp8_linear) g_linear = nullptr;
+decltype(&svdq_fp8_linear_shared) g_linear = nullptr;
+decltype(&svdq_fp8_linear_workspace_bytes) g_linear_bytes = nullptr;
 decltype(&svdq_rope) g_rope = nullptr;
 decltype(&svdq_attention) g_attention = nullptr;
 
@@ -127,6 +129,13 @@ struct Call {
       refuse(SVDQ_ERR_ARG, where, "the last dimension of %s is not contiguous", what);
     return static_cast<uint16_t*>(t.data_ptr());
   }
+  // a workspace: bytes, or None
+  void* memory(PyObject* o, size_t* bytes) const {
+    if (o == Py_None) return nullptr;
+    const at::Tensor& w = tensor(o, "workspace");
+    *bytes = (size_t)w.numel();
+    return *bytes ? plain(o, "workspace", at::kByte, w.sizes()) : nullptr;
+  }
   void* stream(PyObject* o) const {
     if (o == Py_None) return c10::hip::getCurrentHIPStream((c10::DeviceIndex)dev).stream();
     PyObject* a = PyObject_GetAttrString(o, "cuda_stream");
@@ -226,10 +235,24 @@ PyObject* add_rmsnorm_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (xq, xs, wq, ws, Y, bias, stream)
+// Memory of torch's allocator for the length of a call: handed out and taken
+// back in the order of the call's own stream, so later work there may reuse it.
+struct Scratch {
+  void* p = nullptr;
+  Scratch(size_t bytes, void* stream) {
+    if (bytes) p = c10::hip::HIPCachingAllocator::raw_alloc_with_stream(bytes, static_cast<hipStream_t>(stream));
+  }
+  ~Scratch() {
+    if (p) c10::hip::HIPCachingAllocator::raw_delete(p);
+  }
+  Scratch(const Scratch&) = delete;
+  Scratch& operator=(const Scratch&) = delete;
+};
+
+// (xq, xs, wq, ws, Y, bias, workspace, stream); workspace None: torch's, for the call
 PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const char* where = "svdq_fp8_linear";
-  return guarded(where, n, 7, [&] {
+  return guarded(where, n, 8, [&] {
     Call c{where};
     const at::Tensor& Y = c.first(a[4], "Y", 2);
     const at::Tensor &xq = c.tensor(a[0], "xq"), &wq = c.tensor(a[2], "wq");
@@ -245,8 +268,13 @@ PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* bp = static_cast<uint16_t*>(c.optional(a[5], "bias", c.own, {N}));
     c.whole(Y, "Y");
     auto* yp = static_cast<uint16_t*>(Y.data_ptr());
-    void* st = c.stream(a[6]);
-    c.done(without_gil([&] { return g_linear(xp, sp, wp, tp, bp, M, K, N, c.dtype, yp, st); }));
+    size_t bytes = 0;
+    void *own = c.memory(a[6], &bytes), *st = c.stream(a[7]);
+    if (a[6] == Py_None) bytes = g_linear_bytes(M, K, N);
+    const Scratch scratch(a[6] == Py_None ? bytes : 0, st);
+    c.done(without_gil([&] {
+      return g_linear(xp, sp, wp, tp, bp, M, K, N, c.dtype, yp, scratch.p ? scratch.p : own, bytes, st);
+    }));
   });
 }
 
@@ -325,26 +353,21 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if ((a[11] == Py_None) != (a[12] == Py_None)) refuse(SVDQ_ERR_ARG, where, "q_doc and k_doc go together");
     p.q_doc = static_cast<int32_t*>(c.optional(a[11], "q_doc", at::kInt, {p.B, p.Sq}));
     p.k_doc = static_cast<int32_t*>(c.optional(a[12], "k_doc", at::kInt, {p.B, p.Skv}));
-    void* ws = nullptr;
     size_t bytes = 0;
-    if (a[4] != Py_None) {
-      const at::Tensor& w = c.tensor(a[4], "workspace");
-      bytes = (size_t)w.numel();
-      if (bytes) ws = c.plain(a[4], "workspace", at::kByte, w.sizes());
-    }
-    void* st = c.stream(a[13]);
+    void *ws = c.memory(a[4], &bytes), *st = c.stream(a[13]);
     c.done(without_gil([&] { return g_attention(&p, ws, bytes, st); }));
   });
 }
 
-// (SvdqError, address of svdq_add_rmsnorm_quantize, svdq_fp8_linear, svdq_rope, svdq_attention)
+// (SvdqError, addresses of svdq_add_rmsnorm_quantize, svdq_fp8_linear_shared, svdq_fp8_linear_workspace_bytes,
+// svdq_rope, svdq_attention)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind: an exception type and four addresses");
+  if (n != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind: an exception type and five addresses");
     return nullptr;
   }
-  void* at[4];
-  for (int i = 0; i < 4; ++i) {
+  void* at[5];
+  for (int i = 0; i < 5; ++i) {
     at[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (!at[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
@@ -353,8 +376,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   g_norm = reinterpret_cast<decltype(g_norm)>(at[0]);
   g_linear = reinterpret_cast<decltype(g_linear)>(at[1]);
-  g_rope = reinterpret_cast<decltype(g_rope)>(at[2]);
-  g_attention = reinterpret_cast<decltype(g_attention)>(at[3]);
+  g_linear_bytes = reinterpret_cast<decltype(g_linear_bytes)>(at[2]);
+  g_rope = reinterpret_cast<decltype(g_rope)>(at[3]);
+  g_attention = reinterpret_cast<decltype(g_attention)>(at[4]);
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);
   Py_RETURN_NONE;

@@ -137,3 +137,59 @@ def test_stream_and_refusals():
         a.update(change)
         with pytest.raises(B.SvdqError):
             B.fp8_linear(**a)
+
+
+SHARED = [(129, 12288, 1552), (700, 8320, 1552), (2900, 16384, 144), (333, 12416, 3088), (128, 12288, 3072)]
+
+
+@pytest.mark.parametrize("M,K,N", SHARED)
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+def test_blocks_sharing_k(M, K, N, kind):
+    """Uneven parts and ragged edges; a used, larger workspace and torch's own give the same bits."""
+    xq, xs, wq, ws = _operands(M, K, N, M + K + N, "normal")
+    ws *= np.float32(2.0**-14)
+    bd, bv = device(np.random.default_rng(3).standard_normal(N), kind)
+    y, mag = O.fp8_linear(xq, xs, wq, ws, bv)
+    n = B.fp8_linear_workspace_bytes(M, K, N)
+    assert n > 0
+    Y = _run(xq, xs, wq, ws, kind, bd)
+    _check(Y, y, mag, K, kind, f"{kind} {M}x{K}x{N}")
+    t = lambda a: torch.from_numpy(a).cuda()
+    a = dict(xq=t(xq), xs=t(xs), wq=t(wq), ws=t(ws), bias=bd)
+    for w in (torch.full((n + 1024,), 255, dtype=torch.uint8, device="cuda"), None):
+        Y2 = torch.full_like(Y, float("nan"))
+        B.fp8_linear(Y=Y2, workspace=w, **a)
+        assert torch.equal(Y, Y2)
+    with pytest.raises(B.SvdqError):
+        B.fp8_linear(Y=Y2, workspace=w or torch.empty(n - 16, dtype=torch.uint8, device="cuda"), **a)
+    with pytest.raises(B.SvdqError):
+        B.fp8_linear(Y=Y2, workspace=torch.empty(n, dtype=torch.int8, device="cuda"), **a)
+
+
+def test_blocks_sharing_k_on_two_streams_and_in_a_graph():
+    M, K, N = 129, 12288, 1552
+    t = lambda a: torch.from_numpy(a).cuda()
+    ops = [[t(a) for a in _operands(M, K, N, seed, "normal")] for seed in (1, 2)]
+    want = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in ops]
+    for o, y in zip(ops, want):
+        B.fp8_linear(*o, y)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    got = [[torch.zeros_like(want[0]) for _ in range(4)] for _ in ops]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for o, y, s in zip(ops, got, streams):
+            B.fp8_linear(*o, y[i], stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for ys, w in zip(got, want) for y in ys)
+    g, out = torch.cuda.CUDAGraph(), [torch.zeros_like(w) for w in want]
+    with torch.cuda.graph(g):
+        for o, y in zip(ops, out):
+            B.fp8_linear(*o, y)
+    for _ in range(3):
+        for y in out:
+            y.zero_()
+        g.replay()
+        B.fp8_linear(*ops[0], got[0][0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, w) for y, w in zip(out, want))

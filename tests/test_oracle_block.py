@@ -139,6 +139,22 @@ def test_fp8_linear_refusals(change, status):
                                    a["Y"], None) == status
 
 
+def test_fp8_linear_workspace_and_its_refusals():
+    need = B.fp8_linear_workspace_bytes
+    assert need(333, 12288, 3072) == 7 * 3 * 24 * 128 * 128 * 4
+    assert all(need(M, K, N) == 0 for M, K, N in [(0, 12288, 3072), (333, 12300, 3072), (333, 12288, 3080), (1, 128, 16),
+                                                  (1, 12288, 3072), (333, 4096, 3072), (8192, 12288, 3072)])
+    for M in (1, 100, 128, 129, 333, 1000, 2049, 5000, 1 << 18):
+        for K in (128, 6144, 8192, 12288, 16384):
+            for N in (16, 400, 3072, 4112, 65536):
+                assert need(M, K, N) <= 32 << 20
+    a = dict(xq=P, xs=P, wq=P, ws=P, bias=P, M=333, K=12288, N=3072, dtype=1, Y=P, w=P, n=need(333, 12288, 3072))
+    for change, status in [(dict(w=None), ARG), (dict(n=a["n"] - 1), WORKSPACE), (dict(w=P + 4), ALIGN),
+                           (dict(xs=None), ARG), (dict(bias=P + 2), ALIGN), (dict(dtype=2), UNSUPPORTED),
+                           (dict(M=0), SHAPE), (dict(M=1, w=None, n=0, Y=None), ARG)]:
+        assert B.lib().svdq_fp8_linear_shared(*{**a, **change}.values(), None) == status, change
+
+
 def _rope_args(**change):
     a = BB.RopeArgs(4, 3, 16, 64, 1, 0, P, P, P)
     a.x[0] = a.y[0] = a.x[1] = a.y[1] = P
