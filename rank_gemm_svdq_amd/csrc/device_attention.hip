@@ -737,12 +737,12 @@ Plan plan_of(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_
     // share of the keys and about 6 tiles' worth of start and end, and the join.
     // (Against as many parts as fill the chip: 2 x 700 queries of 16 heads on
     // 3001 keys, 68 for 73 us; 1024 of 24 on 4096, 78 for 95; 2500 of 16 on as
-    // many, 93 for 87.)
+    // many, 81 for 87.)
     const int64_t t = ((int64_t)Skv + 63) / 64;
     int64_t best = 0;
     for (int64_t k = 1; k <= most; ++k) {
       const int64_t rounds = (blocks * k + fill - 1) / fill;
-      const int64_t cost = 2 * rounds * ((t + k - 1) / k + 6) + (k > 1 ? 8 + k : 0);
+      const int64_t cost = 2 * rounds * ((t + k - 1) / k + 6) + (k > 1 ? 12 + 3 * k : 0);
       if (k == 1 || cost < best) {
         best = cost;
         s = k;
