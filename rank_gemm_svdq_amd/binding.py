@@ -1,4 +1,5 @@
-"""ctypes binding of libsvdq (include/svdq.h).
+"""Binding of libsvdq (include/svdq.h): ctypes, and the module _block
+(csrc/py_block.cpp) for the operators around the layer.
 
 Argument marshalling only: every step of the layer runs in the C++ host code
 or the HIP kernels of the library.  Host arrays are numpy arrays; device

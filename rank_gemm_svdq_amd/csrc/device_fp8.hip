@@ -462,17 +462,17 @@ bool fp8_sizes(int32_t M, int32_t K, int32_t N) {
 // can still be filled with (256 compute units), and where they are few, waves
 // take the steps of k in turn.  Measured, us (tile side or sides, groups):
 //   M x K x N          row   few   32/8  32x64/4  64/4   64/2   128/1
-//   1 x 3072 x 9216    7.4   8.4                  12.3
-//   16 x 3072 x 9216         12.5  13.4           12.5
-//   64 x 1024 x 1024         3.1   4.3            6.7    6.0    12.1
-//   64 x 12288 x 3072        41    17     27      37     43     115
-//   128 x 12288 x 3072       80    32     27      36     43     116
-//   64 x 3072 x 9216         32    18     18      12.8   13.7   32
-//   256 x 3072 x 3072        42    17     17      12.5   13.5   32
-//   333 x 12288 x 3072       208   78     78      73     66     115
-//   512 x 4096 x 4096        141   50     39      30     28     41
-//   1024 x 3072 x 9216       469   184    136     98     82     72
-//   4096 x 3072 x 9216                                   311    214
+//   1 x 3072 x 9216    7.2   8.3   11    15       11     11     28
+//   16 x 3072 x 9216         12.4  12.4  15       11     12     28
+//   64 x 1024 x 1024         3.1   3.8   4.5      5.8    5.4    11
+//   64 x 12288 x 3072        42    18    27       37     42     100
+//   128 x 12288 x 3072       80    32    27       35     41     101
+//   64 x 3072 x 9216         32    17    17       12.3   13.3   28
+//   256 x 3072 x 3072        41    17    16       11.9   12.9   28
+//   333 x 12288 x 3072       208   77    77       69     59     100
+//   512 x 4096 x 4096        141   48    37       29     25     37
+//   1024 x 3072 x 9216       468   175   126      92     83     68
+//   4096 x 3072 x 9216                                   297    214
 template <int DT>
 svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const uint16_t* bias,
                        int M, int K, int N, uint16_t* Y, hipStream_t st) {
@@ -495,7 +495,10 @@ svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, co
                        xq, xs, wq, ws, bias, M, K, N, Y, tm, tn, 1, nullptr);
   };
   if (M == 1) {
-    if (N >= 6144) row(I2{});   // 3072 -> 9216: 7.3 us against 7.7 with one row; 12288 -> 3072: 9.1 against 8.4
+    // two rows against one, us: 5120 -> 13824 13.2 / 13.6, 3072 -> 9216 7.1 / 7.5,
+    // 3072 -> 5120 5.0 / 4.9, 8192 -> 4096 8.9 / 8.3, 3072 -> 2048 3.2 / 3.0
+    // (12288 -> 3072 the other way, 8.8 / 9.2)
+    if (N >= 6144) row(I2{});
     else row(I1{});
   } else if (M <= 16 || blocks(16, 16) <= 256) {
     hipLaunchKernelGGL((fp8_few_kernel<DT>), dim3(N / 16, (M + 15) / 16), dim3(512), 0, st, xq, xs, wq, ws, bias, M, K,
