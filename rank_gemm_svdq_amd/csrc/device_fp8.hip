@@ -128,10 +128,10 @@ __global__ __launch_bounds__(64 * WN * WM * WK, 2) void fp8_tile_kernel(
     voff[j] = (uint32_t)row * (uint32_t)K + 16u * (slot ^ f);
   }
   const uint32_t lds0 = lds_address(lds);
-  // scales: lane l the wave's token l (its 16 MT; the others repeat)
+  // scales: lane l the wave's token l (its 16 MT; the others repeat one)
   const int m_wave = m0 + 16 * MT * wm;
   const uint8_t* sbase = reinterpret_cast<const uint8_t*>(xs + (size_t)min(m_wave, M - 1) * steps);
-  const uint32_t svoff = (uint32_t)max(min(lane & (16 * MT - 1), M - 1 - m_wave), 0) * (uint32_t)steps * 4u;
+  const uint32_t svoff = (uint32_t)max(min(lane < 16 * MT ? lane : 0, M - 1 - m_wave), 0) * (uint32_t)steps * 4u;
   auto copy = [&](int v) __attribute__((always_inline)) {   // the v-th of this group's steps
     const int t = v * WK + first;
     const uint32_t dst = lds0 + (v & 1) * T::STEP + u0 * 1024;
@@ -434,11 +434,12 @@ __global__ __launch_bounds__(256) void fp8_row_kernel(const uint8_t* __restrict_
 //   12288  27 -> 22      35 -> 30      59 -> 39      61 -> 47      68 -> 57
 //   16384  31 -> 25      44 -> 35      74 -> 46      76 -> 58      90 -> 76
 // (M x N in the head.)  16 tiles lose at any K (100 x 16384 -> 2048 20 -> 25),
-// and so do few tokens (64 x 12288 -> 3072 17.5 -> 21.7).
+// and so do few tokens (64 x 12288 -> 3072 17.5 -> 21.7),
+// and two parts (700 x 12288 -> 4096, 192 tiles: 79 -> 88).
 int64_t fp8_tiles(int M, int N) { return (int64_t)((M + 127) / 128) * ((N + 127) / 128); }
 int fp8_parts(int M, int K, int N) {
   const int64_t tiles = fp8_tiles(M, N), steps = K / 128;
-  if (M <= 64 || steps < 64 || tiles < 24 || tiles > kCus || 2 * tiles + 3 * steps < 336) return 1;
+  if (M <= 64 || steps < 64 || tiles < 24 || tiles > 2 * kCus / 3 || 2 * tiles + 3 * steps < 336) return 1;
   return (int)(2 * kCus / tiles);                            // at most 21
 }
 
@@ -459,9 +460,11 @@ bool fp8_sizes(int32_t M, int32_t K, int32_t N) {
 }
 
 // The variant of a call, by its sizes.  Tiles are taken as large as the chip
-// can still be filled with (256 compute units), and where they are few, waves
-// take the steps of k in turn.  Measured, us (tile side or sides, groups):
-//   M x K x N          row   few   32/8  32x64/4  64/4   64/2   128/1
+// can still be filled with: in one round with a block a compute unit (256),
+// whose groups of waves take the steps of k in turn, or with two.  A larger
+// tile moves fewer bytes per product, but a second round that is mostly empty
+// costs more.  Measured, us (tokens x out-features of a tile / groups):
+//   M x K x N          row   few   32/8  64x32/4  64/4   64/2   128/1
 //   1 x 3072 x 9216    7.2   8.3   11    15       11     11     28
 //   16 x 3072 x 9216         12.4  12.4  15       11     12     28
 //   64 x 1024 x 1024         3.1   3.8   4.5      5.8    5.4    11
@@ -469,16 +472,25 @@ bool fp8_sizes(int32_t M, int32_t K, int32_t N) {
 //   128 x 12288 x 3072       80    32    27       35     41     101
 //   64 x 3072 x 9216         32    17    17       12.3   13.3   28
 //   256 x 3072 x 3072        41    17    16       11.9   12.9   28
-//   333 x 12288 x 3072       208   77    77       69     59     100
-//   512 x 4096 x 4096        141   48    37       29     25     37
-//   1024 x 3072 x 9216       468   175   126      92     83     68
-//   4096 x 3072 x 9216                                   297    214
+//
+//   M x K x N           64/4   64/2   96x128/2  128/2  96x128/1  128/1
+//   512 x 4096 x 4096   26.3   23.7   28.1      32.7   32.0      37.2
+//   200 x 3072 x 9216   29.9   25.5   22.1      25.8   24.6      28.6
+//   900 x 3072 x 3072   30.8   27.4   23.5      26.8   25.7      29.8
+//   1024 x 3072 x 3072  31.0   27.6   42.4      26.5   36.9      29.4
+//   1024 x 4096 x 4096  50.0   44.9   52.0      36.3   46.7      39.1
+//   1500 x 3072 x 3072  48.6   41.0   41.0      50.6   37.5      43.7
+//   512 x 3072 x 9216   48.5   40.8   41.3      49.9   38.5      43.3
+//   1024 x 3072 x 9216  87.1   75.9   80.5      73.9   71.4      67.1
+//   2048 x 3072 x 9216  170    141    139       124    124       112
+//   4096 x 3072 x 9216         297                               214
 template <int DT>
 svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const uint16_t* bias,
                        int M, int K, int N, uint16_t* Y, hipStream_t st) {
   using std::integral_constant;
   typedef integral_constant<int, 1> I1;
   typedef integral_constant<int, 2> I2;
+  typedef integral_constant<int, 3> I3;
   typedef integral_constant<int, 4> I4;
   typedef integral_constant<int, 8> I8;
   auto blocks = [&](int bm, int bn) { return (int64_t)((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
@@ -509,8 +521,14 @@ svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, co
     tile(I2{}, I2{}, I1{}, I2{}, I4{});
   } else if (blocks(64, 64) <= 256) {
     tile(I2{}, I2{}, I2{}, I2{}, I4{});
-  } else if (blocks(64, 64) <= 1280) {
+  } else if (blocks(64, 64) <= 512) {
     tile(I2{}, I2{}, I2{}, I2{}, I2{});
+  } else if (blocks(96, 128) <= 256) {
+    tile(I4{}, I3{}, I2{}, I2{}, I2{});
+  } else if (blocks(128, 128) <= 256) {
+    tile(I4{}, I4{}, I2{}, I2{}, I2{});
+  } else if (blocks(96, 128) <= 512) {
+    tile(I4{}, I3{}, I2{}, I2{}, I1{});
   } else {
     tile(I4{}, I4{}, I2{}, I2{}, I1{});
   }

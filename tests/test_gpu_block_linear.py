@@ -75,6 +75,21 @@ def test_each_arrangement_at_ragged_sizes(M, K, N):
     assert torch.equal(Y, _run(xq, xs, wq, ws, "bf16", bd)), "two runs differ"
 
 
+@pytest.mark.parametrize("M,K,N", [
+    (690, 1152, 2960),                              # 96 x 128 tiles, two groups
+    (1010, 640, 3088),                              # 128 x 128, two groups
+    (1500, 1152, 3088),                             # 96 x 128
+    (2300, 640, 3088)])                             # 128 x 128
+def test_large_tiles_at_ragged_sizes(M, K, N):
+    xq, xs, wq, ws = _operands(M, K, N, M + K + N)
+    bd, bv = device(np.random.default_rng(4).standard_normal(N), "fp16")
+    ws *= np.float32(2.0**-16)
+    y, mag = O.fp8_linear(xq, xs, wq, ws, bv)
+    Y = _run(xq, xs, wq, ws, "fp16", bd)
+    _check(Y, y, mag, K, "fp16", f"{M}x{K}x{N}")
+    assert torch.equal(Y, _run(xq, xs, wq, ws, "fp16", bd)), "two runs differ"
+
+
 def test_every_row_and_column_is_its_own():
     """One nonzero code in each operand: exactly one output is nonzero, for places all over a ragged shape."""
     M, K, N = 270, 512, 656
