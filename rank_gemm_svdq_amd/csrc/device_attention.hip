@@ -25,10 +25,10 @@
 // The maximum is raised only when a tile's exceeds it by more than 8 (in
 // powers of two): the weights stay below 2^8 and the rescaling of O is rare.
 //
-// Two arrangements.  More than 32 rows: the four waves of a block take 128
-// rows and share tiles of 64 keys.  At most 32 rows (a few new tokens): the
-// waves share the rows and take tiles of 32 keys in turn, each with its own
-// buffers and no barriers, and are joined at the end.  Where blocks are few,
+// Two arrangements.  Many rows: the four waves of a block take 128 rows and
+// share tiles of 64 keys.  Few rows (a few new tokens, short prompts): the waves
+// share 32 rows and take tiles of 32 keys in turn, each with its own buffers
+// and no barriers, and are joined at the end.  Where blocks are few,
 // the keys are split over blocks too; a second kernel joins the parts.
 //
 // What bounds it.  Many rows: power and the serial chain of a wave's tile
@@ -718,20 +718,39 @@ Plan plan_of(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_
   p.G = Hq / Hkv;
   p.R = Sq * p.G;
   p.groups = B * Hkv;
-  p.keys = p.R <= 32;
-  p.tiles = p.keys ? 1 : (p.R + 127) / 128;
+  // Blocks of 32 rows whose waves share the keys, as long as the chip holds one
+  // for every 32 rows (LDS: one a compute unit for heads above 64, two below) and
+  // a pass over the keys for 32 rows instead of 128 is not what takes the time.
+  // Measured, us (128 rows -> 32): 512 queries on as many keys, 8 heads of 128
+  // 16.3 -> 11.1; 16 on 8192, 32 on 8 heads 29.6 -> 17.7; 2 x 64 on 512, 16 on
+  // 4 16.9 -> 11.1; 200 on 3000, 8 heads (168000 keys) 22.0 -> 25.5; 6 x 16 on
+  // 11453, 8 on 1 (275000 keys) 33.6 -> 40.5; 4 x 142 on 142, 16 on 2 (288
+  // blocks) 10.7 -> 14.7.
+  const int64_t fine = (int64_t)((p.R + 31) / 32) * p.groups;
+  p.keys = p.R <= 32 || (fine <= (D <= 64 ? 2 : 1) * kCus && fine * Skv <= 160 * 1024);
+  p.tiles = p.keys ? (p.R + 31) / 32 : (p.R + 127) / 128;
   const int64_t blocks = (int64_t)p.tiles * p.groups;
-  // Blocks that the chip holds, and the keys that are worth a block of their own.
+  // Blocks that the chip holds (twice, where LDS allows one a compute unit), and
+  // the keys that are worth a block of their own.
   const int64_t fill = 2 * kCus, least = 512;
   int64_t most = ((int64_t)Skv + least - 1) / least;
   if (most > 64) most = 64;
   int64_t s = 1;
   if (p.keys) {
-    // as many as fill the chip (one request of 8192 keys x 8 K/V heads: 15.5
-    // us; with 1024 keys a part 18.0 us, with 128 20.7 us.  8 of them: 58 us;
-    // with twice the blocks 65 us)
-    s = (fill + blocks - 1) / blocks;
-    if (s > most) s = most;
+    // The least time, in steps of 128 keys (32 a wave): rounds of blocks, each
+    // with its share of the keys and about a step of start and end, and the join.
+    // The most parts among those within 8 %, as lengths may differ.  (One
+    // request of 8192 keys x 8 K/V heads 15.5 us: with 1024 keys a part 18.0,
+    // with 128 20.7.  Against as many parts as fill the chip twice: 3 such
+    // requests 27 for 32 us, 5 of them 41 for 48, 16 of 2048 keys 33 for 37.)
+    const int64_t t = ((int64_t)Skv + 127) / 128, slots = (D <= 64 ? 2 : 1) * kCus;
+    if (most > (fill + blocks - 1) / blocks) most = (fill + blocks - 1) / blocks;
+    auto cost = [&](int64_t k) { return (blocks * k + slots - 1) / slots * ((t + k - 1) / k + 1) + (k > 1); };
+    int64_t best = cost(1);
+    for (int64_t k = 2; k <= most; ++k)
+      if (cost(k) < best) best = cost(k);
+    for (int64_t k = 2; k <= most; ++k)
+      if (cost(k) * 100 <= best * 108) s = k;
   } else if (blocks < fill) {
     // the least time, in half tiles of 64 keys: rounds of blocks, each with its
     // share of the keys and about 6 tiles' worth of start and end, and the join.
@@ -750,7 +769,6 @@ Plan plan_of(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_
     }
   }
   p.splits = s < 1 ? 1 : (int)s;
-  (void)D;
   return p;
 }
 int padded_dim(int32_t D) { return D <= 64 ? 64 : 128; }

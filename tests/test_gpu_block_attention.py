@@ -65,7 +65,12 @@ SHAPES = [  # B, Sq, Skv, Hq, Hkv, D
     (1, 127, 200, 4, 1, 104), (1, 129, 257, 2, 1, 64), (2, 200, 511, 2, 2, 128), (1, 300, 300, 7, 7, 120), (1, 513, 700, 1, 1, 128)]
 
 
-@pytest.mark.parametrize("shape", SHAPES)
+# blocks of 128 rows: enough of them, or many rows times keys (the last: in parts)
+MANY = [(13, 129, 131, 8, 8, 64), (7, 129, 257, 8, 8, 128), (6, 129, 200, 16, 8, 104), (2, 513, 520, 16, 16, 40),
+        (1, 700, 2100, 4, 4, 64)]
+
+
+@pytest.mark.parametrize("shape", SHAPES + MANY)
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("mode", ["all", "causal", "causal_cap", "slopes", "len", "docs", "prefix", "everything"])
 def test_against_oracle(shape, kind, mode):
