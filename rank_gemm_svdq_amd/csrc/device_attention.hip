@@ -38,7 +38,7 @@
 // wave with the two row tiles' softmax and MFMAs side by side (one wave a
 // SIMD) took 525 us, eight waves sharing the copies half a tile apart 345 us.
 // One token: the bytes of K and V; 16 requests of 4096 - 16384 keys x 8 heads
-// 132 us, 5.1 TB/s.
+// 135 us, 5.0 TB/s.
 //
 // Hidden keys.  A hidden score is -infinity, its weight 0, and 0 times what V
 // holds there would be NaN if that is not finite.  O is checked at the end:

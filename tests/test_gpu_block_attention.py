@@ -96,7 +96,8 @@ def test_against_oracle(shape, kind, mode):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("Sq,Skv,Hq,Hkv", [(1, 600, 4, 2), (3, 200, 2, 1), (150, 400, 2, 1), (40, 40, 1, 1)])
+@pytest.mark.parametrize("Sq,Skv,Hq,Hkv", [(1, 600, 4, 2), (3, 200, 2, 1), (150, 400, 2, 1), (40, 40, 1, 1),
+                                             (150, 400, 104, 52)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_hidden_keys_may_hold_anything(kind, Sq, Skv, Hq, Hkv, bad):
     """NaN, infinities and the type's lowest value where a query does not look: past kv_len, in other documents,
@@ -138,22 +139,22 @@ def test_no_keys_at_all():
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-@pytest.mark.parametrize("Sq,Skv", [(1, 2000), (200, 200)])
-def test_extreme_scores(kind, Sq, Skv):
+@pytest.mark.parametrize("Sq,Skv,H", [(1, 2000, 2), (200, 200, 2), (200, 200, 160)])
+def test_extreme_scores(kind, Sq, Skv, H):
     """Scores far apart (one key takes all), equal scores, scores whose maximum climbs along the keys and one whose
     exponentials would overflow without the maximum."""
     D = 64
-    (q, qv), (k, kv), (v, vv) = _make(1, Sq, Skv, 2, 1, D, kind, 31)
+    (q, qv), (k, kv), (v, vv) = _make(1, Sq, Skv, H, H // 2, D, kind, 31)
     for gain in (40.0, 0.0, 1e-3):
         _check(_gpu(q, k, v, scale=gain), qv, kv, vv, kind, f"scale {gain}", scale=gain)
-    up = np.linspace(0, 1, Skv)[None, :, None, None] * np.ones((1, Skv, 1, D))
+    up = np.linspace(0, 1, Skv)[None, :, None, None] * np.ones((1, Skv, H // 2, D))
     kd, kdv = device(up, kind)
-    qd, qdv = device(np.ones((1, Sq, 2, D)), kind)
+    qd, qdv = device(np.ones((1, Sq, H, D)), kind)
     for scale in (4.0, -4.0):
         _check(_gpu(qd, kd, v, scale=scale), qdv, kdv, vv, kind, f"climbing {scale}", scale=scale)
     _check(_gpu(q, k, v, softcap=0.25, scale=40.0), qv, kv, vv, kind, "cap", softcap=0.25, scale=40.0)
     # scores of tens of thousands below zero everywhere: no row is empty
-    sl = [200.0, 100.0]
+    sl = [200.0, 100.0] * (H // 2)
     _check(_gpu(q, k, v, slopes=sl, kv_len=[Skv]), qv, kv, vv, kind, "far", slopes=sl, kv_len=[Skv])
     qdoc, kdoc = np.zeros((1, Sq), np.int32), np.ones((1, Skv), np.int32)
     kdoc[0, 0] = 0                                  # the farthest key is the only one
@@ -185,6 +186,18 @@ def test_strides(kind, Sq):
     _check(o2[1:], values(q)[1:], kv[0][1:, :Skv - 11], kv[1][1:, :Skv - 11], kind, "heads outermost, shorter", **want)
 
 
+def test_strides_of_many_rows():
+    B_, Sq, Skv, Hq, Hkv, D = 3, 140, 150, 64, 32, 64
+    qkv, x = device(np.random.default_rng(42).standard_normal((B_, Skv, Hq + 2 * Hkv, D)), "bf16")
+    q, k, v = qkv[:, Skv - Sq:, :Hq], qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:]
+    kt, vt = (t.transpose(1, 2).contiguous().transpose(1, 2) for t in (k, v))
+    for a, b in ((k, v), (kt, vt)):
+        o = torch.zeros((B_, Sq, Hq, 2 * D), dtype=q.dtype, device="cuda")
+        B.attention(q, a, b, o[..., D:], B.attention_workspace(q, a), causal=True)
+        _check(o[..., D:], values(q), values(k), values(v), "bf16", "columns", causal=True)
+        assert not o[..., :D].any()
+
+
 def test_broadcast_keys():
     """One batch entry's K and V for all (stride 0)."""
     (q, qv), (k, kv), (v, vv) = _make(3, 4, 50, 2, 1, 64, "bf16", 51)
@@ -192,7 +205,7 @@ def test_broadcast_keys():
     _check(_gpu(q, ke, ve), qv, np.repeat(kv[:1], 3, 0), np.repeat(vv[:1], 3, 0), "bf16", "broadcast")
 
 
-@pytest.mark.parametrize("Sq", [1, 100])
+@pytest.mark.parametrize("Sq", [1, 100, 16500])
 def test_offsets_past_32_bits(Sq):
     """Keys more than 2^32 bytes apart."""
     D, Skv = 64, 150
@@ -203,7 +216,8 @@ def test_offsets_past_32_bits(Sq):
     kb.copy_(k)
     vb.copy_(v)
     assert (Skv - 1) * step * 2 > 1 << 32
-    _check(_gpu(q, kb, vb, causal=True), qv, kv, vv, "bf16", "far apart", causal=True)
+    causal = Sq <= Skv
+    _check(_gpu(q, kb, vb, causal=causal), qv, kv, vv, "bf16", "far apart", causal=causal)
 
 
 def test_long_cache_on_sampled_heads():

@@ -62,7 +62,7 @@ def test_against_oracle(M, K, N, kind):
 
 
 @pytest.mark.parametrize("M,K,N", [
-    (2300, 384, 2320), (1283, 1152, 4144),          # 128 x 128 tiles, ragged both ways, odd steps
+    (2300, 384, 2320), (1283, 1152, 4144),          # 96 x 128 tiles, ragged both ways, odd steps
     (333, 2176, 3088), (200, 1152, 2064),           # 64 x 64, waves in two and four turns
     (70, 4224, 1040), (20, 65536, 144), (40, 8320, 2048),   # 64 x 32 and 32 x 32; the largest K
     (1, 65536, 16), (1, 128, 16), (1, 640, 8192), (9, 65536, 32)])
