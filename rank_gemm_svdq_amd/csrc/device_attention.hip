@@ -282,13 +282,17 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
       const int d = 16 * s + 8 * half;
       qf[s] = (b4i){0, 0, 0, 0};
       if (!PAD || d < a.D) qf[s] = *reinterpret_cast<const b4i*>(qp + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (p.flip) qf[s][i] ^= (int)0x80008000;
-        if (p.qmul == 0.f) qf[s][i] = 0;
-      }
     }
   }
+  // its sign, or zero; after the first copies are on their way, as it waits for Q
+  auto turn_q = [&]() __attribute__((always_inline)) {
+    if (p.qmul > 0.f) return;
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[s][i] = p.flip ? qf[s][i] ^ (int)0x80008000 : 0;
+  };
   const int qd = use_docs ? a.q_doc[(size_t)b * a.Sq + qi] : 0;
   int doc_lo = qd, doc_hi = qd;   // documents of the block's rows
   if (!KEYS && use_docs) {
@@ -511,6 +515,7 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     // each wave on its own: tiles t_begin + wave, + 4, ...
     int t = t_begin + wave, buf = 0;
     if (t < t_end) copy_tile(t, 0);
+    turn_q();
     int kd = doc_of(t);
     for (; t < t_end; t += 4, buf ^= 1) {
       dma_wait();
@@ -558,6 +563,7 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     };
     int t = next(t_begin), buf = 0;
     if (t < t_end) copy_tile(t, 0);
+    turn_q();
     int kd = doc_of(t);
     while (t < t_end) {
       // tile t has landed for every wave, and all are done with the one before
