@@ -61,7 +61,8 @@ struct Part {               // how the keys are split over blocks
 struct AttnP {
   svdq_attention_args a;
   int G, R, tiles, groups;  // heads per K/V head, rows per (entry, K/V head), row tiles, entries x K/V heads
-  float qmul, c1, c2, c3;   // see launch()
+  float qmul, c1, c2, c3, c4;   // see svdq_attention()
+  float cap[7];                 // c1 x the coefficients of tanh(x) / x in x^2
   bool flip;
   Part part;
 };
@@ -112,10 +113,35 @@ __device__ __forceinline__ void group_order(const AttnP& p, int* grp, int* rest)
   }
 }
 
-// Score in powers of two of a raw dot product (times scale > 0, cap and bias).
-__device__ __forceinline__ float capped(const AttnP& p, float s) {
-  // cap tanh(s scale / cap) = cap - 2 cap / (e^(2 s scale / cap) + 1), times log2 e
+// Capped score in powers of two of a raw dot product s: cap tanh(x) log2 e with
+// x = s scale / cap, scale > 0, in one of two forms.
+//   by_exp    cap - 2 cap / (e^2x + 1): five instructions, but a difference of two
+//             numbers of the cap's size, so the score is off by up to 2e-7 cap
+//             whatever its own size.
+//   by_series s (scale log2 e) tanh(x) / x, the quotient a polynomial of degree 6
+//             in x^2 (minimax on |x| <= 1, 5.6e-8 relative); beyond, by_exp, whose
+//             error there is 3e-7 of the result.  As exact under a cap of 1e30 as
+//             without one.
+// Caps up to kSmallCap take by_exp: its error is then below 1.3e-5, that of the
+// weight 2^-16, and the 16-bit weights are off by 2^-11 or 2^-8 anyway.
+// The series is slower (2 x 1000 causal queries of 16 heads of 128 36.9 against
+// 34.1 us, 4 x 1024 of 8 heads of 64 30.3 against 26.9; the latter under a cap of
+// 2, where tiles need both, 39.4).
+constexpr float kSmallCap = 64.0f;
+constexpr float kTanh[7] = {1.0f,           -0.33332987f,   0.13326409f, -0.053498708f,
+                            0.020359759f,   -0.0062593391f, 0.0010582646f};
+__device__ __forceinline__ float by_exp(const AttnP& p, float s) {
   return fmaf(-2.0f * p.c3, __builtin_amdgcn_rcpf(exp2_(s * p.c2) + 1.0f), p.c3);
+}
+__device__ __forceinline__ float by_series(const AttnP& p, float s) {   // |x| <= 1
+  const float x = s * p.c4, u = x * x;
+  float q = p.cap[6];
+#pragma unroll
+  for (int i = 5; i >= 0; --i) q = fmaf(q, u, p.cap[i]);
+  return s * q;
+}
+__device__ __forceinline__ float capped(const AttnP& p, float s) {
+  return p.a.softcap <= kSmallCap || !(fabsf(s * p.c4) <= 1.0f) ? by_exp(p, s) : by_series(p, s);
 }
 
 constexpr float kLow = -3.402823466e38f;
@@ -437,10 +463,29 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     if (!plain) {
       c = 1.f;
       if (a.softcap > 0.f) {
+        if (a.softcap <= kSmallCap) {
 #pragma unroll
-        for (int k = 0; k < KT; ++k)
+          for (int k = 0; k < KT; ++k)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[k][i] = capped(p, s[k][i]);
+            for (int i = 0; i < 16; ++i) s[k][i] = by_exp(p, s[k][i]);
+        } else {
+          float big = 0.f;
+#pragma unroll
+          for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) big = fmaxf(big, fabsf(s[k][i]));
+          if (__any(big * p.c4 > 1.0f)) {
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[k][i] = capped(p, s[k][i]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[k][i] = by_series(p, s[k][i]);
+          }
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < KT; ++k)
@@ -838,8 +883,11 @@ extern "C" svdq_status svdq_attention(const svdq_attention_args* a, void* ws, si
   p.flip = a->scale < 0.f;
   p.qmul = a->scale < 0.f ? -1.f : a->scale > 0.f ? 1.f : 0.f;
   p.c1 = scale * log2e;
-  p.c2 = a->softcap > 0.f ? 2.f * scale / a->softcap * log2e : 0.f;
+  // finite, so that a score of 0 stays 0 under the smallest cap
+  p.c2 = a->softcap > 0.f ? fminf(2.f * scale / a->softcap * log2e, 3.0e38f) : 0.f;
   p.c3 = a->softcap * log2e;
+  p.c4 = a->softcap > 0.f ? fminf(scale / a->softcap, 3.0e38f) : 0.f;
+  for (int i = 0; i < 7; ++i) p.cap[i] = p.c1 * kTanh[i];
   p.part.splits = pl.splits;
   p.part.o = static_cast<float*>(ws);
   p.part.ml = pl.splits > 1
