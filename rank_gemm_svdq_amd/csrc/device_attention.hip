@@ -41,9 +41,14 @@
 // 135 us, 5.0 TB/s.
 //
 // Hidden keys.  A hidden score is -infinity, its weight 0, and 0 times what V
-// holds there would be NaN if that is not finite.  O is checked at the end:
-// rows that came out not finite are computed again key by key, without the
-// hidden ones (row_again).
+// holds there would be NaN if that is not finite.  O is checked at the end of a
+// block's tiles: where a row with a finite sum of weights came out not finite, the
+// block goes over its tiles once more (AGAIN), and each tile's values that are not
+// finite are taken out of LDS and kept as marks of the rows that see them;
+// everything else is worked out as before, so hidden values do not change a bit of
+// the result.  A sum of weights that is not finite needs no second pass: hidden
+// scores do not enter it, so the row is NaN.  (2048 tokens, all visible, 8 heads of
+// 128 46 us, with one NaN in V 94, with nothing else in it 1.7 ms.)
 
 #include "device_block.h"
 
@@ -146,66 +151,18 @@ __device__ __forceinline__ float capped(const AttnP& p, float s) {
 
 constexpr float kLow = -3.402823466e38f;
 
-// One row key by key over [j0, j1), lane l with elements 2 l, 2 l + 1: the
-// maximum, the sum and the weighted values of the visible keys alone.
-template <int DT>
-__device__ __forceinline__ void row_again(const AttnP& p, int b, int hk, int r, int n, int j0, int j1, float* m_out,
-                                          float* l_out, b2f* o_out) {
-  const svdq_attention_args& a = p.a;
-  const int lane = threadIdx.x & 63;
-  const int i = r / p.G, h = hk * p.G + r % p.G;
-  const bool live = 2 * lane < a.D;
-  const int pos = n - a.Sq + i;
-  auto pair = [&](const uint16_t* t) {
-    return live ? widen2<DT>(*reinterpret_cast<const uint32_t*>(t + 2 * lane)) : (b2f){0.f, 0.f};
-  };
-  const b2f q = pair(a.q + b * a.q_batch + i * a.q_token + h * a.q_head);
-  const int end = a.causal ? min(j1, max(pos + 1, a.prefix ? a.prefix[b] : 0)) : j1;
-  float top = kLow, sum = 0.f;
-  b2f o = (b2f){0.f, 0.f};
-  for (int j = j0; j < end; ++j) {
-    if (a.q_doc && a.k_doc[(size_t)b * a.Skv + j] != a.q_doc[(size_t)b * a.Sq + i]) continue;
-    const b2f k = pair(a.k + b * a.k_batch + j * a.k_token + hk * a.k_head);
-    float s = fmaf(q[0], k[0], q[1] * k[1]);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
-    s *= p.qmul;
-    s = a.softcap > 0.f ? capped(p, s) : s * p.c1;
-    if (a.slopes) s -= a.slopes[h] * 1.44269504f * fabsf((float)(pos - j));
-    const float up = fmaxf(top, s);
-    const float f = exp2_(top - up), w = exp2_(s - up);
-    const b2f v = pair(a.v + b * a.v_batch + j * a.v_token + hk * a.v_head);
-    sum = fmaf(sum, f, w);
-    o[0] = fmaf(o[0], f, w * v[0]);
-    o[1] = fmaf(o[1], f, w * v[1]);
-    top = up;
-  }
-  *m_out = top;
-  *l_out = sum;
-  *o_out = o;
-}
-
 // The end of 32 rows of a wave (lane l: row row0 + l % 32, O^T as the MFMAs
-// leave it, m and l of the whole row): rows that are not finite are computed
-// again over keys [j0, j1), the others stored, as parts or finished.
+// leave it, m and l of the whole row): stored as parts or finished.
 template <int DT, int DP, bool PAD>
-__device__ __forceinline__ void store_rows(const AttnP& p, int grp, int b, int hk, int sp, int n, int row0, int j0,
-                                           int j1, float m, float l, const b16f (&o)[DP / 32]) {
+__device__ __forceinline__ void store_rows(const AttnP& p, int grp, int b, int hk, int sp, int row0, float m, float l,
+                                           const b16f (&o)[DP / 32]) {
   const svdq_attention_args& a = p.a;
   constexpr int ND = DP / 32;
   const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
-  const int row = min(row0 + l32, p.R - 1);
-  bool bad = !(fabsf(l) < __builtin_inff());
-#pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) bad = bad || !(fabsf(o[d][i]) < __builtin_inff());
-  const bool real = row0 + l32 < p.R;
-  const uint64_t who = __ballot(bad && real);
-  const uint32_t again = (uint32_t)(who | (who >> 32));
+  const int row = row0 + l32;
   const size_t rows_all = (size_t)p.groups * p.R;
   const bool parts = p.part.splits > 1;
-  if (real && !((again >> l32) & 1)) {
+  if (row < p.R) {
     if (parts) {
       const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + row;
       float* op = p.part.o + at * DP;
@@ -231,44 +188,45 @@ __device__ __forceinline__ void store_rows(const AttnP& p, int grp, int b, int h
         }
     }
   }
-  for (uint32_t left = again; left; left &= left - 1) {
-    const int r = row0 + __builtin_ctz(left);
-    float rm, rl;
-    b2f ro;
-    row_again<DT>(p, b, hk, r, n, j0, j1, &rm, &rl, &ro);
-    if (parts) {
-      const size_t at = (size_t)sp * rows_all + (size_t)grp * p.R + r;
-      if (2 * lane < DP) *reinterpret_cast<b2f*>(p.part.o + at * DP + 2 * lane) = ro;
-      if (lane == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * at) = make_float2(rm, rl);
-    } else if (2 * lane < a.D) {
-      const float by = rl != 0.f ? 1.0f / rl : 0.f;
-      uint16_t* op = a.o + b * a.o_batch + (r / p.G) * a.o_token + (hk * p.G + r % p.G) * a.o_head;
-      *reinterpret_cast<uint32_t*>(op + 2 * lane) = narrow2<DT>(ro[0] * by, ro[1] * by);
-    }
-  }
 }
 
-// KEYS: waves share 32 rows and take key tiles in turn; otherwise waves take
-// rows and share key tiles.  PAD: D < DP.
-template <int DT, int DP, bool PAD, bool KEYS>
-__global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_kernel(AttnP p) {
+// LDS of a block.  KEYS: waves share 32 rows and take key tiles in turn; otherwise
+// waves take rows and share key tiles.
+template <int DP, bool KEYS>
+struct Shared {
+  static constexpr int KT = KEYS ? 1 : 2;          // 32-key subtiles of a tile
+  static constexpr int TK = 32 * KT;
+  static constexpr int TILE = TK * 2 * DP;         // one of K, V
+  static constexpr int RING = 4 * TILE;            // K, V of two tiles
+  static constexpr int LDS = KEYS ? 4 * RING : RING;
+  __attribute__((aligned(1024))) uint8_t tiles[LDS];
+  int docs[4][TK];
+  uint32_t seen[KEYS ? 1 : kSeen / 32];
+  uint32_t redo[4];                                // per wave: rows for the second pass
+  uint32_t marks[DP / 32][256];                    // per lane, two bits per register of O: it saw +, - infinity (NaN: both)
+};
+
+// A block's rows over its share of the keys.  PAD: D < DP.  AGAIN: without values
+// that are not finite, weights up to 2^lag.  Returns whether rows have to be gone over
+// again, and stores them if not.
+template <int DT, int DP, bool PAD, bool KEYS, bool AGAIN>
+__device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>* sh, float lag) {
   const svdq_attention_args& a = p.a;
-  constexpr int KT = KEYS ? 1 : 2;                 // 32-key subtiles of a tile
-  constexpr int TK = 32 * KT;
+  using S = Shared<DP, KEYS>;
+  constexpr int KT = S::KT, TK = S::TK, TILE = S::TILE, RING = S::RING, LDS = S::LDS;
   constexpr int ROWB = 2 * DP;                     // bytes of a row in LDS
-  constexpr int TILE = TK * ROWB;                  // one of K, V
   constexpr int CH = DP / 8;                       // 16-byte chunks of a row
   constexpr int RPI = 64 / CH;                     // rows of one 1 KB copy
   constexpr int COPIES = TILE / 1024;              // of K or V, per tile
   constexpr int MINE = KEYS ? COPIES : COPIES / 4; // per wave
   constexpr int NS = DP / 16;                      // MFMA steps of S
   constexpr int ND = DP / 32;                      // 32-column tiles of O
-  constexpr int AHEAD_K = 4, AHEAD_V = 2;        // fragments read ahead
-  constexpr int RING = 4 * TILE;                   // K, V of two tiles
-  constexpr int LDS = KEYS ? 4 * RING : RING;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
-  __shared__ int docs[4][TK];
-  __shared__ uint32_t seen[KEYS ? 1 : kSeen / 32];
+  constexpr int AHEAD_K = 4, AHEAD_V = 2;          // fragments read ahead
+  uint8_t* lds = sh->tiles;
+  auto& docs = sh->docs;
+  auto& seen = sh->seen;
+  auto& redo = sh->redo;
+  auto& marks = sh->marks;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -396,12 +354,8 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     for (int d = 0; d < ND; ++d) voff[d] = kr * ROWB + 16 * v_chunk(kr, 4 * d) + 32 * dh + 8 * (i16 % 4);
   }
 
-  float m = kLow, l = 0.f;
+  float m, l;
   b16f o[ND];
-#pragma unroll
-  for (int d = 0; d < ND; ++d)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
   const bool plain = !(a.softcap > 0.f) && !a.slopes;   // score = c1 x dot product
 
@@ -528,7 +482,7 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[k][i]);
     top = half_max(top) * c;
-    if (__any(top > m + 8.0f)) {
+    if (__any(top > m + lag)) {
       const float up = fmaxf(m, top);
       const float f = exp2_(m - up);
       m = up;
@@ -556,6 +510,97 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     return use_docs && t < t_end ? a.k_doc[(size_t)b * a.Skv + min(t * TK + (lane & (TK - 1)), n - 1)] : 0;
   };
 
+  // Second pass, tile t in `buf` before its scores: the keys whose values are not
+  // all finite are found, each lane marks those values of its columns that its
+  // row sees, and they are set to zero.  All waves find the same keys.
+  auto take_out = [&](int t, int buf, int kd) __attribute__((always_inline)) {
+    constexpr uint32_t EXP = DT == SVDQ_BF16 ? 0x7F80u : 0x7C00u;   // all ones: infinity or NaN
+    uint8_t* vt = lds + (KEYS ? wave * RING : 0) + buf * 2 * TILE + TILE;
+    auto odd = [&](uint32_t w) { return (w & EXP) == EXP || ((w >> 16) & EXP) == EXP; };
+    // KEYS: a lane looks through half a key; otherwise through one
+    constexpr int LOOK = KEYS ? CH / 2 : CH;
+    const int key = lane & (TK - 1);               // its chunks in another order than its neighbours', for the banks
+    uint8_t* own = vt + key * ROWB + (KEYS ? half * (ROWB / 2) : 0);
+    bool any = false;
+#pragma unroll 1
+    for (int c = 0; c < LOOK; ++c) {
+      const b4i w = *reinterpret_cast<const b4i*>(own + 16 * ((c + key) % LOOK));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) any = any || odd((uint32_t)w[i]);
+    }
+    uint64_t keys = __ballot(any);
+    if (KEYS) keys = (keys | (keys >> 32)) & 0xFFFFFFFFull;
+    if (keys == 0) return;
+#pragma unroll 1
+    for (uint64_t left = keys; left; left &= left - 1) {
+      const int j = __builtin_ctzll(left);
+      const uint32_t sees = t * TK + j < lim && (!use_docs || __builtin_amdgcn_readlane(kd, j) == qd) ? ~0u : 0u;
+#pragma unroll 1
+      for (int c = 0; c < 4 * ND; ++c) {
+        const uint2 w = *reinterpret_cast<const uint2*>(vt + j * ROWB + 16 * v_chunk(j, c) + 8 * half);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = (i < 2 ? w.x : w.y) >> (16 * (i & 1)) & 0xFFFFu;
+          const uint32_t kind = (v & 0x7FFFu) > EXP ? 3u : v & 0x8000u ? 2u : 1u;
+          if ((v & EXP) == EXP) bits |= kind << (2 * i);
+        }
+        marks[c >> 2][threadIdx.x] |= (bits & sees) << (8 * (c & 3));
+      }
+    }
+    // every wave that reads these values has marked them
+    if constexpr (KEYS) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      __syncthreads();
+    }
+    if (KEYS || key / 16 == wave) {
+#pragma unroll 1
+      for (int c = 0; c < LOOK; ++c) {
+        b4i w = *reinterpret_cast<const b4i*>(own + 16 * ((c + key) % LOOK));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t v = (uint32_t)w[i];
+          if ((v & EXP) == EXP) v &= 0xFFFF0000u;
+          if (((v >> 16) & EXP) == EXP) v &= 0x0000FFFFu;
+          w[i] = (int)v;
+        }
+        *reinterpret_cast<b4i*>(own + 16 * ((c + key) % LOOK)) = w;
+      }
+    }
+    if constexpr (KEYS) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+    } else {
+      __syncthreads();
+    }
+  };
+
+  // documents: which tiles the block has to visit (see below)
+  if (!KEYS && use_docs) {
+    for (int w = wave; w < (min(t_end - t_begin, kSeen) + 31) / 32; w += 4) {
+      int kd[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const int j = (t_begin + 32 * w + k) * TK + lane;
+        kd[k] = a.k_doc[(size_t)b * a.Skv + min(j, n - 1)];
+      }
+      uint32_t bits = 0;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) bits |= (__any(kd[k] >= doc_lo && kd[k] <= doc_hi) ? 1u : 0u) << k;
+      if (lane == 0) seen[w] = bits;
+    }
+    __syncthreads();
+  }
+
+  m = kLow;
+  l = 0.f;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+
   if constexpr (KEYS) {
     // each wave on its own: tiles t_begin + wave, + 4, ...
     int t = t_begin + wave, buf = 0;
@@ -567,6 +612,7 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
       __builtin_amdgcn_wave_barrier();
       if (t + 4 < t_end) copy_tile(t + 4, buf ^ 1);
       const int kd_next = doc_of(t + 4);
+      if constexpr (AGAIN) take_out(t, buf, kd);
       scores(t, buf, kd);
       values(buf);
       // this tile's LDS reads end before the next copy may overwrite it
@@ -575,23 +621,8 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
     }
   } else {
     // Tiles in turn; where documents are used, those that hold none of the
-    // block's are passed over: the waves look through the first kSeen tiles of
-    // the block's share beforehand (later ones are all visited).
-    if (use_docs) {
-      for (int w = wave; w < (min(t_end - t_begin, kSeen) + 31) / 32; w += 4) {
-        int kd[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int j = (t_begin + 32 * w + k) * TK + lane;
-          kd[k] = a.k_doc[(size_t)b * a.Skv + min(j, n - 1)];
-        }
-        uint32_t bits = 0;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) bits |= (__any(kd[k] >= doc_lo && kd[k] <= doc_hi) ? 1u : 0u) << k;
-        if (lane == 0) seen[w] = bits;
-      }
-      __syncthreads();
-    }
+    // block's are passed over: the waves have looked through the first kSeen tiles
+    // of the block's share beforehand (later ones are all visited).
     int word = -1;
     uint32_t bits = 0;
     auto next = [&](int t) -> int {
@@ -617,6 +648,7 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
       const int tn = next(t + 1);
       if (tn < t_end) copy_tile(tn, buf ^ 1);
       const int kd_next = doc_of(tn);
+      if constexpr (AGAIN) take_out(t, buf, kd);
       if (t * TK < lim_last) {
         scores(t, buf, kd);
         values(buf);
@@ -626,12 +658,11 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
       buf ^= 1;
     }
   }
-
   l = half_sum(l);
 
   if constexpr (KEYS) {
-    // join the waves: O^T, m and l of waves 1..3 through LDS (their buffers
-    // are no longer needed), wave 0 goes on alone
+    // join the waves: O^T, m and l of waves 1..3 through LDS, where the tiles were,
+    // to wave 0
     __syncthreads();
     float* jo = reinterpret_cast<float*>(lds);                 // [4][32 rows][DP + 4]
     float* jm = reinterpret_cast<float*>(lds) + 4 * 32 * (DP + 4);
@@ -648,33 +679,91 @@ __global__ __launch_bounds__(256, (KEYS && DP == 128) ? 1 : 2) void attention_ke
               (b4f){o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
     }
     __syncthreads();
-    if (wave > 0) return;
-    float up = m;
+    if (wave == 0) {
+      float up = m;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) up = fmaxf(up, jm[(w * 32 + l32) * 2]);
-    const float f0 = exp2_(m - up);
-    l *= f0;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= f0;
-#pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      const float f = exp2_(jm[(w * 32 + l32) * 2] - up);
-      l = fmaf(f, jm[(w * 32 + l32) * 2 + 1], l);
+      for (int w = 1; w < 4; ++w) up = fmaxf(up, jm[(w * 32 + l32) * 2]);
+      const float f0 = exp2_(m - up);
+      l *= f0;
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const b4f x = *reinterpret_cast<const b4f*>(jo + (w * 32 + l32) * (DP + 4) + 32 * d + 8 * g + 4 * half);
+        for (int i = 0; i < 16; ++i) o[d][i] *= f0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[d][4 * g + i] = fmaf(f, x[i], o[d][4 * g + i]);
-        }
+      for (int w = 1; w < 4; ++w) {
+        const float f = exp2_(jm[(w * 32 + l32) * 2] - up);
+        l = fmaf(f, jm[(w * 32 + l32) * 2 + 1], l);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const b4f x = *reinterpret_cast<const b4f*>(jo + (w * 32 + l32) * (DP + 4) + 32 * d + 8 * g + 4 * half);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[d][4 * g + i] = fmaf(f, x[i], o[d][4 * g + i]);
+          }
+      }
+      m = up;
     }
-    m = up;
   }
 
-  store_rows<DT, DP, PAD>(p, grp, b, hk, sp, n, row0, t_begin * TK, min(n, t_end * TK), m, l, o);
+  // Rows to be gone over again?  (KEYS: wave 0 has them all.)  A sum over O tells in
+  // half the instructions of a look at each; should it overflow, the passes are
+  // only in vain.
+  bool odd = false;
+  if (!KEYS || wave == 0) {
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i % 4] += o[d][i];
+    odd = !(fabsf(sum[0] + sum[1] + (sum[2] + sum[3])) < __builtin_inff()) && fabsf(l) < __builtin_inff() &&
+          row0 + l32 < p.R;
+  }
+  uint32_t rows = __any(odd);
+  if (lane == 0) redo[wave] = rows;
+  __syncthreads();
+  if (!KEYS || wave > 0) rows = __builtin_amdgcn_readfirstlane(redo[0] | redo[1] | redo[2] | redo[3]);
+  if (__builtin_expect(rows != 0 && lag != 0.f, 0)) return true;
+  if (KEYS && wave > 0) return false;
+  if constexpr (AGAIN) {
+    // O is finite where it is marked: add the infinity or NaN
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      uint32_t bits = marks[d][threadIdx.x];
+      if (KEYS) bits |= marks[d][64 + lane] | marks[d][128 + lane] | marks[d][192 + lane];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t plus = bits >> (2 * i) & 1u, minus = bits >> (2 * i + 1) & 1u;
+        o[d][i] += __uint_as_float((plus | minus) * 0x7F800000u | (plus & minus) << 22 | (minus & ~plus) << 31);
+      }
+    }
+  }
+
+  store_rows<DT, DP, PAD>(p, grp, b, hk, sp, row0, m, l, o);
+  return false;
+}
+
+// The second pass, and a third with weights up to 1 should sums of finite values
+// overflow, start from the arguments, read again through an address that the
+// compiler does not know: with anything kept for them from the first (as a loop
+// around both would) calls took 0.4 - 0.8 us more.  Three blocks of 128 rows of
+// heads up to 64 fit a compute unit by the first pass' registers; the bound keeps
+// the rare one from taking more.
+template <int DT, int DP, bool PAD, bool KEYS>
+__global__ __launch_bounds__(256, KEYS && DP == 128 ? 1 : KEYS || DP == 128 ? 2 : 3) void attention_kernel(AttnP p) {
+  __shared__ Shared<DP, KEYS> sh;
+  if (__builtin_expect(attention_block<DT, DP, PAD, KEYS, false>(p, &sh, 8.0f), 0)) {
+    uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    const AttnP again = *(const AttnP*)(__attribute__((address_space(4))) const AttnP*)at;
+#pragma unroll 1
+    for (float lag = 8.0f;; lag = 0.f) {
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d) sh.marks[d][threadIdx.x] = 0;
+      if (!attention_block<DT, DP, PAD, KEYS, true>(again, &sh, lag)) break;
+    }
+  }
 }
 
 // Joins the parts of the rows: DP / 8 lanes hold a row's 8-element pieces, and
