@@ -385,9 +385,9 @@ typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_FP16 = 1 } svdq_dtype;
  * fp32 sum of squares in the same way.)
  * x, residual, h: device [M, K] with row strides (multiples of 8 elements, at
  * least K); residual may be NULL (h = x) and so may h (not stored).  h may be
- * x or residual itself.  weight: device [K].  q: device [M, K] bytes, s:
- * device [M, ceil(K / 128)], both contiguous: the operand of
- * svdq_fp8_linear where K % 128 == 0.
+ * x or residual itself, with the same stride; other overlap is not allowed.
+ * weight: device [K].  q: device [M, K] bytes, s: device [M, ceil(K / 128)],
+ * both contiguous: the operand of svdq_fp8_linear where K % 128 == 0.
  * 1 <= M <= 2^20, 8 <= K <= 65536, K % 8 == 0; eps >= 0 and finite.
  * Errors: ARG, SHAPE, ALIGN (16 bytes; s: 4 bytes), UNSUPPORTED, DEVICE. */
 svdq_status svdq_add_rmsnorm_quantize(const uint16_t* x, int64_t x_stride, const uint16_t* residual,

@@ -573,7 +573,7 @@ def _block():
 def add_rmsnorm_quantize(x, weight, eps, q, s, residual=None, h=None, stream=None):
     """svdq_add_rmsnorm_quantize: h = x + residual, y = h / rms(h) * weight,
     q, s = y in E4M3 with an fp32 scale per 128 columns.  x, residual, h:
-    [M, K] (rows may be strided; h may be x or residual); weight [K];
+    [M, K] (rows may be strided; h may be x or residual, strides alike); weight [K];
     q [M, K] float8_e4m3fn or uint8; s [M, ceil(K / 128)] float32.  Writes q, s
     and, if given, h."""
     (_blk or _block()).add_rmsnorm_quantize(x, weight, eps, q, s, residual, h, stream)

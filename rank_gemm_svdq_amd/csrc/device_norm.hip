@@ -142,6 +142,10 @@ extern "C" svdq_status svdq_add_rmsnorm_quantize(const uint16_t* x, int64_t x_st
   if (x_stride < K || (residual && residual_stride < K) || (h && h_stride < K)) return SVDQ_ERR_SHAPE;
   if (x_stride % 8 != 0 || (residual && residual_stride % 8 != 0) || (h && h_stride % 8 != 0)) return SVDQ_ERR_ALIGN;
   if (!on16(x) || !on16(residual) || !on16(weight) || !on16(h) || !on16(q) || !on4(s)) return SVDQ_ERR_ALIGN;
+  // in place, element for element: with another stride rows would be written that
+  // are still to be read
+  if (h && M > 1 && ((h == x && h_stride != x_stride) || (h == residual && h_stride != residual_stride)))
+    return SVDQ_ERR_ARG;
   const svdq_status ok = device_ok();
   if (ok != SVDQ_OK) return ok;
   hipStream_t st = static_cast<hipStream_t>(stream);

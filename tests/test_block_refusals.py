@@ -1,0 +1,16 @@
+"""More refusals of the block operators' C entries (CPU: every argument is
+checked before any device call; the pointers are never followed)."""
+import pytest
+
+import rank_gemm_svdq_amd as B
+
+P, Q = 1 << 20, 1 << 24     # aligned addresses
+ARG = 1
+
+
+@pytest.mark.parametrize("change", [dict(h=P, hst=256), dict(h=P, xst=256), dict(h=Q, hst=256, rst=128), dict(h=Q, rst=136)])
+def test_norm_in_place_with_another_stride(change):
+    a = dict(x=P, xst=128, r=Q, rst=128, w=P, eps=1e-6, M=4, K=128, dtype=0, h=P, hst=128, q=P, s=P)
+    a.update(change)
+    assert B.lib().svdq_add_rmsnorm_quantize(a["x"], a["xst"], a["r"], a["rst"], a["w"], a["eps"], a["M"], a["K"],
+                                             a["dtype"], a["h"], a["hst"], a["q"], a["s"], None) == ARG
