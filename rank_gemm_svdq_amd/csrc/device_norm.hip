@@ -16,9 +16,10 @@
 namespace svdq {
 namespace {
 
+// h may lie where x or res does (a lane reads its chunks of both before it stores
+// any), so neither is restrict.
 template <int DT, int NC>
-__global__ __launch_bounds__(1024) void norm_kernel(const uint16_t* __restrict__ x, int64_t xst,
-                                                    const uint16_t* __restrict__ res, int64_t rst,
+__global__ __launch_bounds__(1024) void norm_kernel(const uint16_t* x, int64_t xst, const uint16_t* res, int64_t rst,
                                                     const uint16_t* __restrict__ wt, float eps, int M, int K,
                                                     uint16_t* h, int64_t hst, uint8_t* __restrict__ q,
                                                     float* __restrict__ s, int W) {
