@@ -381,8 +381,8 @@ typedef enum svdq_dtype { SVDQ_BF16 = 0, SVDQ_FP16 = 1 } svdq_dtype;
  * whose s is below 2^-126 gets s = 0 and zero codes.  A block that holds a
  * NaN gets s = NaN, zero codes for its finite values and NaN codes for the
  * rest; an infinity anywhere in a row makes the row's norm infinite, so
- * the other values of the row become 0.  (|h| above about 1e19 overflows the
- * fp32 sum of squares in the same way.)
+ * the other values of the row become 0.  Finite rows of any magnitude have
+ * their norm (rows whose squares leave fp32 are scaled by a power of two).
  * x, residual, h: device [M, K] with row strides (multiples of 8 elements, at
  * least K); residual may be NULL (h = x) and so may h (not stored).  h may be
  * x or residual itself, with the same stride; other overlap is not allowed.

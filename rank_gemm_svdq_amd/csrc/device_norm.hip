@@ -49,7 +49,6 @@ __global__ __launch_bounds__(1024) void norm_kernel(const uint16_t* x, int64_t x
     const int k = first + c * stride;
     wv[c] = k < chunks ? *reinterpret_cast<const b4i*>(wt + 8 * (size_t)k) : (b4i){0, 0, 0, 0};
   }
-  float sum = 0.f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     widen8<DT>(xv[c], v[c]);
@@ -61,18 +60,37 @@ __global__ __launch_bounds__(1024) void norm_kernel(const uint16_t* x, int64_t x
     }
     const int k = first + c * stride;
     if (h && k < chunks) *reinterpret_cast<b4i*>(h + (size_t)row * hst + 8 * (size_t)k) = narrow8<DT>(v[c]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(v[c][i], v[c][i], sum);
   }
+  auto squares = [&]() {   // of the row
+    float sum = 0.f;
 #pragma unroll
-  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  if (W > 1) {
-    if (lane == 0) part[wave] = sum;
-    __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < W; ++i) sum += part[i];
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(v[c][i], v[c][i], sum);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (W > 1) {
+      if (lane == 0) part[wave] = sum;
+      __syncthreads();
+      sum = 0.f;
+      for (int i = 0; i < W; ++i) sum += part[i];
+    }
+    return sum;
+  };
+  float mean = squares() / (float)K + eps;
+  // The squares of bf16 values leave fp32 above 2^64 and below 2^-63.  Such rows,
+  // whole or with a mean that small, are scaled by 2^-90 or 2^90 (exactly; their
+  // squares are in range then) and summed again: y does not change with h's scale.
+  if (DT == SVDQ_BF16 && !(mean >= 0x1p-80f && mean < __builtin_inff())) {
+    const float by = mean < 1.f ? 0x1p90f : 0x1p-90f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= by;
+    if (W > 1) __syncthreads();
+    mean = squares() / (float)K + eps * by * by;
   }
-  const float inv = 1.0f / sqrtf(sum / (float)K + eps);
+  const float inv = 1.0f / sqrtf(mean);
   const int blocks = (K + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK;
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
