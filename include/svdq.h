@@ -429,9 +429,10 @@ svdq_status svdq_fp8_linear_shared(const uint8_t* xq, const float* xs, const uin
  * or with `shared` != 0 one ladder through all pairs, e = 2 j / sum(dims).
  * Writes, for all sum(dims) / 2 pairs, turns[2 j] + turns[2 j + 1] =
  * theta^-e / (2 pi) as an fp32 value and its remainder, and axis[j].
- * dims, turns, axis: host.  Errors: ARG (NULL, theta not finite or not
- * positive), SHAPE (axes outside 1..SVDQ_ROPE_MAX_AXES, an odd or negative
- * dims[a], sum(dims) not a multiple of 16 or outside 16..512). */
+ * dims, turns, axis: host.
+ * Errors: ARG (NULL; theta not finite, not positive, or so small that a
+ * frequency reaches 2^103 turns), SHAPE (axes outside 1..SVDQ_ROPE_MAX_AXES, an
+ * odd or negative dims[a], sum(dims) not a multiple of 16 or outside 16..512). */
 svdq_status svdq_rope_frequencies(int32_t axes, const int32_t* dims, double theta, int32_t shared, float* turns,
                                   int32_t* axis);
 

@@ -19,6 +19,7 @@ extern "C" svdq_status svdq_rope_frequencies(int32_t axes, const int32_t* dims, 
     for (int i = 0; i < dims[a] / 2; ++i, ++j) {
       const double e = shared ? 2.0 * j / (double)total : 2.0 * i / (double)dims[a];
       const double f = std::pow(theta, -e) / two_pi;
+      if (!(f < 0x1p103)) return SVDQ_ERR_ARG;   // times a position below 2^24: within fp32
       const float hi = (float)f;
       turns[2 * j] = hi;
       turns[2 * j + 1] = (float)(f - (double)hi);

@@ -1,5 +1,6 @@
 """More refusals of the block operators' C entries (CPU: every argument is
 checked before any device call; the pointers are never followed)."""
+import numpy as np
 import pytest
 
 import rank_gemm_svdq_amd as B
@@ -14,3 +15,16 @@ def test_norm_in_place_with_another_stride(change):
     a.update(change)
     assert B.lib().svdq_add_rmsnorm_quantize(a["x"], a["xst"], a["r"], a["rst"], a["w"], a["eps"], a["M"], a["K"],
                                              a["dtype"], a["h"], a["hst"], a["q"], a["s"], None) == ARG
+
+
+@pytest.mark.parametrize("dims,theta", [([16], 1e-300), ([16, 112], 1e-33), ([64], 5e-324)])
+def test_frequencies_beyond_fp32(dims, theta):
+    """A position below 2^24 times a frequency has to stay finite."""
+    with pytest.raises(B.SvdqError) as e:
+        B.rope_frequencies(dims, theta)
+    assert e.value.status == ARG
+
+
+def test_the_largest_frequencies_are_finite():
+    turns, _ = B.rope_frequencies([16, 112], 1e-31)
+    assert np.isfinite(turns).all() and np.isfinite(turns * np.float32((1 << 24) - 1)).all()
