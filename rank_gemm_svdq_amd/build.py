@@ -5,6 +5,7 @@ Host sources are compiled with g++ (x86-64-v3, no fp contraction in the
 packers), device sources with hipcc for gfx950; hipcc links the library.
 """
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -53,7 +54,10 @@ def _ext_command(out):
 
 
 def build_ext():
-    """Compile the marshalling module in-tree (lib/_block.so)."""
+    """Compile the marshalling module in-tree (lib/_block.so).  Without torch,
+    whose tensors it takes, there is nothing to build: the C library stands alone."""
+    if importlib.util.find_spec("torch") is None:
+        return None
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = EXT + ".tmp"
     _run(_ext_command(tmp))
@@ -114,8 +118,9 @@ def build(verbose=False, sanitize=False, reuse_device_objects=False):
              ["-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib", "-lpthread"])
     else:
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs + ["-lpthread"])
-        build_ext()
     os.replace(tmp, lib)
+    if not sanitize:
+        build_ext()
     return lib
 
 
