@@ -46,21 +46,23 @@ def _ext_command(out):
     t = os.path.dirname(torch.__file__)
     inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], "/opt/rocm/include"]
-    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wextra", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
-            + [f"-I{d}" for d in inc] + [os.path.join(CSRC, "py_block.cpp"), "-o", out]
+            + [f"-isystem{d}" for d in inc] + [os.path.join(CSRC, "py_block.cpp"), "-o", out]
             + [f"-L{os.path.join(t, 'lib')}", f"-Wl,-rpath,{os.path.join(t, 'lib')}",
                "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip"])
 
 
-def build_ext():
+def build_ext(verbose=False):
     """Compile the marshalling module in-tree (lib/_block.so).  Without torch,
     whose tensors it takes, there is nothing to build: the C library stands alone."""
     if importlib.util.find_spec("torch") is None:
         return None
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = EXT + ".tmp"
-    _run(_ext_command(tmp))
+    out = _run(_ext_command(tmp))
+    if verbose and out:
+        print(out)
     os.replace(tmp, EXT)
     return EXT
 
@@ -120,7 +122,7 @@ def build(verbose=False, sanitize=False, reuse_device_objects=False):
         _run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs + ["-lpthread"])
     os.replace(tmp, lib)
     if not sanitize:
-        build_ext()
+        build_ext(verbose)
     return lib
 
 

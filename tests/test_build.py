@@ -46,3 +46,11 @@ def test_without_torch_there_is_no_module_to_build(recorded, monkeypatch):
     monkeypatch.setitem(sys.modules, "torch", None)
     assert BLD.build() == BLD.LIB
     assert os.path.exists(BLD.LIB) and not os.path.exists(BLD.EXT)
+
+
+def test_the_module_is_compiled_with_its_warnings_on(recorded):
+    """Torch's headers are system headers, so that what is said is said of the module."""
+    _, done = recorded
+    BLD.build()
+    cmd = next(c for c in done if any("py_block.cpp" in a for a in c))
+    assert "-Wall" in cmd and "-Wextra" in cmd and "-w" not in cmd and not any(a.startswith("-I") for a in cmd)
