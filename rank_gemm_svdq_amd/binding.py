@@ -109,6 +109,8 @@ class SearchResult(C.Structure):
                 ("errors", C.c_void_p), ("best_iter", C.c_int32)]
 
 
+# The block operators' argument structures, for callers of lib() (rope() and
+# attention() below fill theirs in C++).
 class RopeArgs(C.Structure):
     _fields_ = ([(n, C.c_int32) for n in ("M", "axes", "pairs", "head_dim", "interleaved", "dtype")]
                 + [(n, C.c_void_p) for n in ("positions", "turns", "axis")]

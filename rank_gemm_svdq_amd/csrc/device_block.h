@@ -14,7 +14,6 @@ namespace svdq {
 namespace {
 
 typedef int b4i __attribute__((ext_vector_type(4)));
-typedef int b8i __attribute__((ext_vector_type(8)));
 typedef float b2f __attribute__((ext_vector_type(2)));
 typedef float b4f __attribute__((ext_vector_type(4)));
 typedef float b16f __attribute__((ext_vector_type(16)));
@@ -96,7 +95,10 @@ __device__ __forceinline__ int xcd_order(int b, int total) {
   return x * q + min(x, r) + (b >> 3);
 }
 
-constexpr int kCus = 256;   // compute units of the chip, for the choice of variants on the host
+// Compute units, for the choice of variants on the host: those of a whole gfx950,
+// not the current device's count, as workspace sizes follow from these choices and
+// are asked for without a device.
+constexpr int kCus = 256;
 
 inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool on4(const void* p) { return ((uintptr_t)p & 3u) == 0; }

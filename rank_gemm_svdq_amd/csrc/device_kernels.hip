@@ -1331,7 +1331,7 @@ __global__ __launch_bounds__(256) void kup_kernel(const uint16_t* __restrict__ z
 // compute units of the current device, cached per device (write-once)
 static std::atomic<int> g_dev_cus[64];
 
-int device_cus() {
+static int device_cus() {
   int dev = 0, v = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
   v = g_dev_cus[dev].load(std::memory_order_relaxed);

@@ -101,9 +101,7 @@ struct CandidateView {
 };
 using Scorer = std::function<svdq_status(const CandidateView&, double* score)>;
 
-// compute units of the current device, and the gfx950 check, both cached per
-// device (device_kernels.hip)
-int device_cus();
+// the gfx950 check of the current device, cached per device (device_kernels.hip)
 svdq_status device_ok();
 
 // svdq_prepare with an optional scorer of the residual iterations.
