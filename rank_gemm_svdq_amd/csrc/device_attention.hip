@@ -48,7 +48,7 @@
 // everything else is worked out as before, so hidden values do not change a bit of
 // the result.  A sum of weights that is not finite needs no second pass: hidden
 // scores do not enter it, so the row is NaN.  (2048 tokens, all visible, 8 heads of
-// 128 46 us, with one NaN in V 94, with nothing else in it 1.7 ms.)
+// 128 46 us, with one NaN in V 83, with nothing else in it 1.7 ms.)
 
 #include "device_block.h"
 
@@ -100,8 +100,7 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // so), and the longest rows of a causal mask then come first in every group
 // (237 against 178 us).
 template <bool KEYS>
-__device__ __forceinline__ void group_order(const AttnP& p, int* grp, int* rest) {
-  const int b = blockIdx.x;
+__device__ __forceinline__ void group_order(const AttnP& p, int b, int* grp, int* rest) {
   if constexpr (KEYS) {
     // nothing is shared between blocks: the parts of a group follow each other
     // (one token of 16 requests: 142 us, 150 the other way)
@@ -154,11 +153,11 @@ constexpr float kLow = -3.402823466e38f;
 // The end of 32 rows of a wave (lane l: row row0 + l % 32, O^T as the MFMAs
 // leave it, m and l of the whole row): stored as parts or finished.
 template <int DT, int DP, bool PAD>
-__device__ __forceinline__ void store_rows(const AttnP& p, int grp, int b, int hk, int sp, int row0, float m, float l,
+__device__ __forceinline__ void store_rows(const AttnP& p, int grp, int b, int hk, int sp, int row0, int lane, float m, float l,
                                            const b16f (&o)[DP / 32]) {
   const svdq_attention_args& a = p.a;
   constexpr int ND = DP / 32;
-  const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+  const int l32 = lane & 31, half = lane >> 5;
   const int row = row0 + l32;
   const size_t rows_all = (size_t)p.groups * p.R;
   const bool parts = p.part.splits > 1;
@@ -206,9 +205,9 @@ struct Shared {
   uint32_t marks[DP / 32][256];                    // per lane, two bits per register of O: it saw +, - infinity (NaN: both)
 };
 
-// A block's rows over its share of the keys.  PAD: D < DP.  AGAIN: without values
-// that are not finite, weights up to 2^lag.  Returns whether rows have to be gone over
-// again, and stores them if not.
+// A block's rows over its share of the keys.  PAD: D < DP.  KEYS: returns whether
+// rows have to be gone over again; the call with AGAIN does that, with weights up to
+// 2^lag.
 template <int DT, int DP, bool PAD, bool KEYS, bool AGAIN>
 __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>* sh, float lag) {
   const svdq_attention_args& a = p.a;
@@ -228,11 +227,13 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
   auto& redo = sh->redo;
   auto& marks = sh->marks;
 
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tid = threadIdx.x, block = blockIdx.x;
+  if constexpr (AGAIN) asm volatile("" : "+v"(tid), "+s"(block));   // see attention_kernel
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, half = lane >> 5;
   int grp, rest;
-  group_order<KEYS>(p, &grp, &rest);
+  group_order<KEYS>(p, block, &grp, &rest);
   // the last rows see most keys under a causal mask: they go first
   const int rt = p.tiles - 1 - rest / p.part.splits, sp = rest % p.part.splits;
   const int b = grp / a.Hkv, hk = grp % a.Hkv;
@@ -300,7 +301,7 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
   if constexpr (PAD) {
     // columns D .. DP of the buffers are never copied: zero for good
     uint32_t* w = reinterpret_cast<uint32_t*>(lds);
-    for (int i = threadIdx.x; i < LDS / 4; i += 256) w[i] = 0;
+    for (int i = tid; i < LDS / 4; i += 256) w[i] = 0;
     __syncthreads();
   }
   const uint8_t* kbase = reinterpret_cast<const uint8_t*>(a.k + b * a.k_batch + hk * a.k_head);
@@ -545,7 +546,7 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
           const uint32_t kind = (v & 0x7FFFu) > EXP ? 3u : v & 0x8000u ? 2u : 1u;
           if ((v & EXP) == EXP) bits |= kind << (2 * i);
         }
-        marks[c >> 2][threadIdx.x] |= (bits & sees) << (8 * (c & 3));
+        marks[c >> 2][tid] |= (bits & sees) << (8 * (c & 3));
       }
     }
     // every wave that reads these values has marked them
@@ -594,71 +595,76 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
     __syncthreads();
   }
 
-  m = kLow;
-  l = 0.f;
+  // One pass over the block's tiles.  SECOND: without what is not finite.
+  auto pass = [&](auto second) __attribute__((always_inline)) {
+    constexpr bool SECOND = decltype(second)::value;
+    m = kLow;
+    l = 0.f;
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+      for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
-  if constexpr (KEYS) {
-    // each wave on its own: tiles t_begin + wave, + 4, ...
-    int t = t_begin + wave, buf = 0;
-    if (t < t_end) copy_tile(t, 0);
-    turn_q();
-    int kd = doc_of(t);
-    for (; t < t_end; t += 4, buf ^= 1) {
-      dma_wait();
-      __builtin_amdgcn_wave_barrier();
-      if (t + 4 < t_end) copy_tile(t + 4, buf ^ 1);
-      const int kd_next = doc_of(t + 4);
-      if constexpr (AGAIN) take_out(t, buf, kd);
-      scores(t, buf, kd);
-      values(buf);
-      // this tile's LDS reads end before the next copy may overwrite it
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      kd = kd_next;
-    }
-  } else {
-    // Tiles in turn; where documents are used, those that hold none of the
-    // block's are passed over: the waves have looked through the first kSeen tiles
-    // of the block's share beforehand (later ones are all visited).
-    int word = -1;
-    uint32_t bits = 0;
-    auto next = [&](int t) -> int {
-      if (!use_docs) return t;
-      for (int i = t - t_begin; i < t_end - t_begin && i < kSeen; i = (i | 31) + 1) {
-        if (i >> 5 != word) {
-          word = i >> 5;
-          bits = __builtin_amdgcn_readfirstlane(seen[word]);
-        }
-        const uint32_t left = bits >> (i & 31);
-        if (left) return min(t_end, t_begin + i + __builtin_ctz(left));
-      }
-      return min(t_end, max(t, t_begin + kSeen));
-    };
-    int t = next(t_begin), buf = 0;
-    if (t < t_end) copy_tile(t, 0);
-    turn_q();
-    int kd = doc_of(t);
-    while (t < t_end) {
-      // tile t has landed for every wave, and all are done with the one before
-      dma_wait();
-      __syncthreads();
-      const int tn = next(t + 1);
-      if (tn < t_end) copy_tile(tn, buf ^ 1);
-      const int kd_next = doc_of(tn);
-      if constexpr (AGAIN) take_out(t, buf, kd);
-      if (t * TK < lim_last) {
+    if constexpr (KEYS) {
+      // each wave on its own: tiles t_begin + wave, + 4, ...
+      int t = t_begin + wave, buf = 0;
+      if (t < t_end) copy_tile(t, 0);
+      turn_q();
+      int kd = doc_of(t);
+      for (; t < t_end; t += 4, buf ^= 1) {
+        dma_wait();
+        __builtin_amdgcn_wave_barrier();
+        if (t + 4 < t_end) copy_tile(t + 4, buf ^ 1);
+        const int kd_next = doc_of(t + 4);
+        if constexpr (SECOND) take_out(t, buf, kd);
         scores(t, buf, kd);
         values(buf);
+        // this tile's LDS reads end before the next copy may overwrite it
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        kd = kd_next;
       }
-      kd = kd_next;
-      t = tn;
-      buf ^= 1;
+    } else {
+      // Tiles in turn; where documents are used, those that hold none of the
+      // block's are passed over: the waves have looked through the first kSeen tiles
+      // of the block's share beforehand (later ones are all visited).
+      int word = -1;
+      uint32_t bits = 0;
+      auto next = [&](int t) -> int {
+        if (!use_docs) return t;
+        for (int i = t - t_begin; i < t_end - t_begin && i < kSeen; i = (i | 31) + 1) {
+          if (i >> 5 != word) {
+            word = i >> 5;
+            bits = __builtin_amdgcn_readfirstlane(seen[word]);
+          }
+          const uint32_t left = bits >> (i & 31);
+          if (left) return min(t_end, t_begin + i + __builtin_ctz(left));
+        }
+        return min(t_end, max(t, t_begin + kSeen));
+      };
+      int t = next(t_begin), buf = 0;
+      if (t < t_end) copy_tile(t, 0);
+      if constexpr (!SECOND) turn_q();
+      int kd = doc_of(t);
+      while (t < t_end) {
+        // tile t has landed for every wave, and all are done with the one before
+        dma_wait();
+        __syncthreads();
+        const int tn = next(t + 1);
+        if (tn < t_end) copy_tile(tn, buf ^ 1);
+        const int kd_next = doc_of(tn);
+        if constexpr (SECOND) take_out(t, buf, kd);
+        if (t * TK < lim_last) {
+          scores(t, buf, kd);
+          values(buf);
+        }
+        kd = kd_next;
+        t = tn;
+        buf ^= 1;
+      }
     }
-  }
-  l = half_sum(l);
+    l = half_sum(l);
+  };
+  pass(std::integral_constant<bool, AGAIN>{});
 
   if constexpr (KEYS) {
     // join the waves: O^T, m and l of waves 1..3 through LDS, where the tiles were,
@@ -709,27 +715,48 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
   // Rows to be gone over again?  (KEYS: wave 0 has them all.)  A sum over O tells in
   // half the instructions of a look at each; should it overflow, the passes are
   // only in vain.
-  bool odd = false;
-  if (!KEYS || wave == 0) {
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  auto any_odd = [&]() __attribute__((always_inline)) -> bool {
+    bool odd = false;
+    if (!KEYS || wave == 0) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+      for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum[i % 4] += o[d][i];
-    odd = !(fabsf(sum[0] + sum[1] + (sum[2] + sum[3])) < __builtin_inff()) && fabsf(l) < __builtin_inff() &&
-          row0 + l32 < p.R;
+        for (int i = 0; i < 16; ++i) sum[i % 4] += o[d][i];
+      odd = !(fabsf(sum[0] + sum[1] + (sum[2] + sum[3])) < __builtin_inff()) && fabsf(l) < __builtin_inff() &&
+            row0 + l32 < p.R;
+    }
+    uint32_t rows = __any(odd);
+    if (lane == 0) redo[wave] = rows;
+    __syncthreads();
+    if (!KEYS || wave > 0) rows = __builtin_amdgcn_readfirstlane(redo[0] | redo[1] | redo[2] | redo[3]);
+    return rows != 0;
+  };
+  // The second pass, and a third with weights up to 1 should sums of finite values
+  // overflow.  KEYS: by the caller.
+  bool marked = AGAIN;
+  if (__builtin_expect(any_odd(), 0)) {
+    if constexpr (KEYS) {
+      if (lag != 0.f) return true;
+    } else {
+#pragma unroll 1
+      for (;;) {
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < ND; ++d) marks[d][tid] = 0;
+        pass(std::true_type{});
+        if (!any_odd() || lag == 0.f) break;
+        lag = 0.f;
+      }
+      marked = true;
+    }
   }
-  uint32_t rows = __any(odd);
-  if (lane == 0) redo[wave] = rows;
-  __syncthreads();
-  if (!KEYS || wave > 0) rows = __builtin_amdgcn_readfirstlane(redo[0] | redo[1] | redo[2] | redo[3]);
-  if (__builtin_expect(rows != 0 && lag != 0.f, 0)) return true;
   if (KEYS && wave > 0) return false;
-  if constexpr (AGAIN) {
+  if (__builtin_expect(marked, KEYS)) {
     // O is finite where it is marked: add the infinity or NaN
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-      uint32_t bits = marks[d][threadIdx.x];
+      uint32_t bits = marks[d][tid];
       if (KEYS) bits |= marks[d][64 + lane] | marks[d][128 + lane] | marks[d][192 + lane];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -739,29 +766,29 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
     }
   }
 
-  store_rows<DT, DP, PAD>(p, grp, b, hk, sp, row0, m, l, o);
+  store_rows<DT, DP, PAD>(p, grp, b, hk, sp, row0, lane, m, l, o);
   return false;
 }
 
-// The second pass, and a third with weights up to 1 should sums of finite values
-// overflow, start from the arguments, read again through an address that the
-// compiler does not know: with anything kept for them from the first (as a loop
-// around both would) calls took 0.4 - 0.8 us more.  Three blocks of 128 rows of
-// heads up to 64 fit a compute unit by the first pass' registers; the bound keeps
-// the rare one from taking more.
+// With KEYS the second pass starts from the arguments, read again through an address
+// that the compiler does not know, as a block does from its place in the grid: with
+// anything kept for it from the first pass short calls took 0.4 - 0.8 us more.  128
+// rows a block keep what they have (starting anew they would need scratch memory).
 template <int DT, int DP, bool PAD, bool KEYS>
-__global__ __launch_bounds__(256, KEYS && DP == 128 ? 1 : KEYS || DP == 128 ? 2 : 3) void attention_kernel(AttnP p) {
+__global__ __launch_bounds__(256, KEYS && DP == 128 ? 1 : 2) void attention_kernel(AttnP p) {
   __shared__ Shared<DP, KEYS> sh;
-  if (__builtin_expect(attention_block<DT, DP, PAD, KEYS, false>(p, &sh, 8.0f), 0)) {
-    uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+s"(at));
-    const AttnP again = *(const AttnP*)(__attribute__((address_space(4))) const AttnP*)at;
+  const bool again = attention_block<DT, DP, PAD, KEYS, false>(p, &sh, 8.0f);
+  if constexpr (KEYS) {
+    if (__builtin_expect(!again, 1)) return;
 #pragma unroll 1
     for (float lag = 8.0f;; lag = 0.f) {
+      uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+      asm volatile("" : "+s"(at));
+      const AttnP q = *(const AttnP*)(__attribute__((address_space(4))) const AttnP*)at;
       __syncthreads();
 #pragma unroll
       for (int d = 0; d < DP / 32; ++d) sh.marks[d][threadIdx.x] = 0;
-      if (!attention_block<DT, DP, PAD, KEYS, true>(again, &sh, lag)) break;
+      if (!attention_block<DT, DP, PAD, KEYS, true>(q, &sh, lag)) return;
     }
   }
 }
