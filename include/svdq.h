@@ -401,8 +401,9 @@ svdq_status svdq_add_rmsnorm_quantize(const uint16_t* x, int64_t x_stride, const
  * svdq_add_rmsnorm_quantize writes them); wq: device [N, K] E4M3 codes, ws:
  * device [ceil(N / 128), K / 128] fp32 (128 x 128 blocks); bias: device [N]
  * or NULL; Y: device [M, N].  bias and Y are of `dtype`; all contiguous.
- * Block sums are formed by the matrix units in fp32, scaled and added in
- * fp32, rounded once on the store.
+ * Block sums are formed by the matrix units in fp32, scaled by xs ws (one fp32
+ * product) and added in fp32, rounded once on the store.  With M = 1 the codes
+ * of x are scaled before the products, which are all added in fp32.
  * The layer's shape rules hold for M, K and N (K % 128 == 0, N % 16 == 0).
  * Errors: ARG, SHAPE, ALIGN (16 bytes; xs, ws: 4 bytes), UNSUPPORTED, DEVICE. */
 svdq_status svdq_fp8_linear(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws,

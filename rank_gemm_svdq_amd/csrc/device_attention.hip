@@ -34,11 +34,14 @@
 // What bounds it.  Many rows: power and the serial chain of a wave's tile
 // (scores 700 cycles, maximum 440, weights 740, values 800 and 560 for the
 // barrier and the copies, two waves a SIMD, at 1.6 - 1.8 GHz under this load):
-// 4608 tokens x 24 heads of 128: 297 us, 880 TFLOP/s; causal 154 us.  64 rows a
+// 4608 tokens x 24 heads of 128: 287 - 300 us, 870 - 910 TFLOP/s; causal 153 us.  64 rows a
 // wave with the two row tiles' softmax and MFMAs side by side (one wave a
 // SIMD) took 525 us, eight waves sharing the copies half a tile apart 345 us.
+// Heads of 64 have half the MFMAs of heads of 128 for the same softmax and are
+// bound by its instructions: 5173 tokens x 24 heads of 64 218 us, 760 TFLOP/s, of
+// 128 357 us, 920.
 // One token: the bytes of K and V; 16 requests of 4096 - 16384 keys x 8 heads
-// 135 us, 5.0 TB/s.
+// 130 - 136 us, 5.0 TB/s.
 //
 // Hidden keys.  A hidden score is -infinity, its weight 0, and 0 times what V
 // holds there would be NaN if that is not finite.  O is checked at the end of a
@@ -94,16 +97,14 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 // Which (entry, K/V head) and which of its row tiles and key parts a block
 // takes.  Blocks are dealt to the 8 XCDs round robin; with a multiple of 8
 // groups an XCD keeps to groups of its own, so that its L2 holds their K and V.
-// Neighbouring blocks take different groups: the rows of one head lie a fixed
-// stride apart, which can put them all on a few of the L2's channels (4608
-// tokens x 24 heads of 128: 350 us with one group after the other, 317 us
-// so), and the longest rows of a causal mask then come first in every group
-// (237 against 178 us).
+// Neighbouring blocks take different groups, so that the longest rows of a causal
+// mask come first in every group (4608 tokens x 24 heads of 128: 152 us, 164 with
+// one group after the other; all visible 295 either way).
 template <bool KEYS>
 __device__ __forceinline__ void group_order(const AttnP& p, int b, int* grp, int* rest) {
   if constexpr (KEYS) {
     // nothing is shared between blocks: the parts of a group follow each other
-    // (one token of 16 requests: 142 us, 150 the other way)
+    // (one token of 16 requests: 136 us, 147 the other way)
     const int id = xcd_order(b, gridDim.x), per = p.tiles * p.part.splits;
     *grp = id / per;
     *rest = id % per;
@@ -503,6 +504,10 @@ __device__ __forceinline__ bool attention_block(const AttnP& p, Shared<DP, KEYS>
         part += s[k][i];
       }
       l += part;
+      // To the product with V the weights go in the call's type, as the matrix unit
+      // takes it; their sum stays as they were.  The output is off by at most 2^-8
+      // (bf16) or 2^-11 (fp16) of mean |v| for that (error against 64 bits 2.3e-3 and
+      // 2.8e-4 of its norm, of which the store 1.7e-3 and 2.1e-4).
 #pragma unroll
       for (int x = 0; x < 8; ++x) pf[2 * k + x / 4][x % 4] = (int)narrow2<DT>(s[k][2 * x], s[k][2 * x + 1]);
     }

@@ -59,9 +59,9 @@ __device__ __forceinline__ void add_bias8(const uint16_t* bias, int n, float* v)
 // next pair run (two sets of them), and the token codes of the next tile are
 // read ahead.  Two waves a SIMD hide most of the widening and scaling behind
 // the other's MFMAs.  4096 x 3072 -> 9216 in 128 x 128 tiles, two blocks a
-// compute unit: 214 us, 1.08 PFLOP/s (a large bf16 product of the vendor's
-// library: 1.21); without the copies it would take 180 us, without the
-// widening 203 us.
+// compute unit: 203 us, 1.14 PFLOP/s (a large bf16 product of the vendor's
+// library: 1.21).  When it took 214 us, timing it without the copies gave 180 us,
+// without the widening 203 us.
 
 template <int NT, int MT, int WN, int WM, int WK>
 struct Tile {
@@ -370,7 +370,8 @@ __global__ __launch_bounds__(512) void fp8_few_kernel(const uint8_t* __restrict_
 // No matrix unit: a wave reads RW weight rows 1 KB at a time (whole lines, 16
 // codes a lane), multiplies them with the token's codes of the same places and
 // keeps one fp32 sum per row and lane; a lane's codes of a kilobyte lie in one
-// scale block.  The lanes are added at the end.  3072 -> 9216: 7.4 us, 3.8 TB/s.
+// scale block.  The lanes are added at the end.  3072 -> 9216: 7.0 - 7.4 us, 3.8 -
+// 4.1 TB/s.
 
 template <int DT, int RW>
 __global__ __launch_bounds__(256) void fp8_row_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ xs,
@@ -435,7 +436,8 @@ __global__ __launch_bounds__(256) void fp8_row_kernel(const uint8_t* __restrict_
 //   16384  31 -> 25      44 -> 35      74 -> 46      76 -> 58      90 -> 76
 // (M x N in the head.)  16 tiles lose at any K (100 x 16384 -> 2048 20 -> 25),
 // and so do few tokens (64 x 12288 -> 3072 17.5 -> 21.7),
-// and two parts (700 x 12288 -> 4096, 192 tiles: 79 -> 88).
+// and two parts (700 x 12288 -> 4096, 192 tiles: 79 -> 88).  The last condition of
+// the rule is a line drawn between the shapes that lose and win above.
 int64_t fp8_tiles(int M, int N) { return (int64_t)((M + 127) / 128) * ((N + 127) / 128); }
 int fp8_parts(int M, int K, int N) {
   const int64_t tiles = fp8_tiles(M, N), steps = K / 128;
@@ -483,7 +485,9 @@ bool fp8_sizes(int32_t M, int32_t K, int32_t N) {
 //   512 x 3072 x 9216   48.5   40.8   41.3      49.9   38.5      43.3
 //   1024 x 3072 x 9216  87.1   75.9   80.5      73.9   71.4      67.1
 //   2048 x 3072 x 9216  170    141    139       124    124       112
-//   4096 x 3072 x 9216         297                               214
+//   4096 x 3072 x 9216         297                               203
+// (At 16 x 3072 x 9216 64/4 is a tenth faster than few, which the rule takes for
+// all of 2 to 16 tokens: 12.4 us, and 11.4 with 17 tokens.)
 template <int DT>
 svdq_status launch_fp8(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, const uint16_t* bias,
                        int M, int K, int N, uint16_t* Y, hipStream_t st) {

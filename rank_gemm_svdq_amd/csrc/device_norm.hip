@@ -8,8 +8,8 @@
 // (7 per element with a residual).  W waves share a row; lane l of them owns
 // the 8-element chunks l, l + 64 W, ... so every load is 16 bytes a lane, and
 // the 16 lanes of one 128-column block are neighbours: its maximum is four
-// lane exchanges.  4096 x 3072 with a residual: 17.4 us, 5.1 TB/s, the rate of
-// a large copy; 8192 x 12288: 124 us, 5.7 TB/s.
+// lane exchanges.  4096 x 3072 with a residual: 17 - 18 us, 4.9 - 5.2 TB/s, the
+// rate of a large copy; 8192 x 12288: 125 us, 5.6 TB/s.
 
 #include "device_block.h"
 
@@ -128,8 +128,8 @@ svdq_status launch_norm(const uint16_t* x, int64_t xst, const uint16_t* res, int
   const int chunks = K / 8;
   // Chunks of a lane.  Few rows: one, so that a row's loads are one round trip
   // (3072 columns: 1 row 3.0 us against 4.0 us with up to four chunks, 256
-  // rows 3.6 against 4.5).  Many rows fill the chip by themselves and fewer,
-  // fuller waves are better (4096 rows 17.4 us against 19.9 us).
+  // rows 3.6 against 4.6).  Many rows fill the chip by themselves and fewer,
+  // fuller waves are better (4096 rows 18.1 us against 20.2 us).
   const int per = M <= 512 ? 1 : 4;
   int W = 1;
   while (W < 16 && 64 * W * per < chunks) W *= 2;

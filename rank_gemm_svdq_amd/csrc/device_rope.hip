@@ -12,7 +12,7 @@
 // over (token, head) pairs with them, four in flight.  A lane owns 8 elements
 // of a head: 4 neighbouring pairs, or 8 firsts and their 8 partners.  Bytes
 // bound it: every element is read and written once.  4608 tokens x 48 heads of
-// 128: 23.4 us, 4.8 TB/s (a large copy: 5.2 TB/s).
+// 128: 22.5 - 23.7 us, 4.8 - 5.0 TB/s (a large copy: 5.2 TB/s).
 
 #include "device_block.h"
 
@@ -164,8 +164,8 @@ extern "C" svdq_status svdq_rope(const svdq_rope_args* a, void* stream) {
   const int per = 256 / p.units;
   if (a->M > 256) {
     // all heads of a token, or of the few tokens that keep every thread at work
-    // (4608 tokens x 48 heads of 128: 24.1 us with one token a block, 25.1 with
-    // four, 29.5 with a third of the heads)
+    // (4608 tokens x 48 heads of 128: 23.7 us with one token a block, 24.8 with
+    // four, 29.1 with a third of the heads)
     const int fill = per / p.heads, most = kTable / p.pairs;
     p.tokens = fill > most ? most : fill > 1 ? fill : 1;
     p.share = p.heads;
