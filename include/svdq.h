@@ -479,7 +479,7 @@ typedef struct svdq_attention_args {
   float softcap;                /* > 0: scores become softcap * tanh(score / softcap); 0: off */
   /* device, element (b, i, h, d) at b * batch + i * token + h * head + d;
    * strides are multiples of 8 elements, k_token and v_token in 0..2^25.  k and
-   * v may be NULL if Skv == 0.  B Hq Sq is at most 2^30. */
+   * v may be NULL if Skv == 0.  B Hq is below 2^24, B Hq Sq at most 2^30. */
   const uint16_t *q, *k, *v;
   uint16_t* o;
   int64_t q_batch, q_token, q_head, k_batch, k_token, k_head, v_batch, v_token, v_head, o_batch, o_token, o_head;

@@ -862,7 +862,8 @@ svdq_status check(const svdq_attention_args* a) {
   if (a->B < 1 || a->Sq < 1 || a->Sq > lim || a->Skv < 0 || a->Skv > lim || a->Hq < 1 || a->Hkv < 1 ||
       a->Hq > 65536 || a->Hq % a->Hkv != 0 || a->D < 8 || a->D > SVDQ_ATTENTION_MAX_HEAD_DIM || a->D % 8 != 0)
     return SVDQ_ERR_SHAPE;
-  if ((int64_t)a->B * a->Hq > (1 << 24) || (int64_t)a->B * a->Hq * a->Sq > (int64_t)1 << 30) return SVDQ_ERR_SHAPE;
+  // at most a block of 256 threads per head and 32 rows: fewer than 2^32 threads
+  if ((int64_t)a->B * a->Hq >= (1 << 24) || (int64_t)a->B * a->Hq * a->Sq > (int64_t)1 << 30) return SVDQ_ERR_SHAPE;
   if (a->Skv > 0 && (!a->k || !a->v)) return SVDQ_ERR_ARG;
   if ((a->q_doc == nullptr) != (a->k_doc == nullptr) && a->Skv > 0) return SVDQ_ERR_ARG;
   const float big = 3.0e38f;
@@ -976,7 +977,7 @@ using namespace svdq;
 extern "C" size_t svdq_attention_workspace_bytes(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv,
                                                  int32_t D) {
   if (B < 1 || Sq < 1 || Skv < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 8 || D > SVDQ_ATTENTION_MAX_HEAD_DIM ||
-      (int64_t)B * Hq > (1 << 24) || (int64_t)B * Hq * Sq > (int64_t)1 << 30)
+      (int64_t)B * Hq >= (1 << 24) || (int64_t)B * Hq * Sq > (int64_t)1 << 30)
     return 0;
   const Plan p = plan_of(B, Sq, Skv, Hq, Hkv, D);
   if (p.splits == 1) return 0;

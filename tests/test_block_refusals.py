@@ -1,12 +1,14 @@
 """More refusals of the block operators' C entries (CPU: every argument is
 checked before any device call; the pointers are never followed)."""
+import ctypes as C
+
 import numpy as np
 import pytest
 
 import rank_gemm_svdq_amd as B
 
 P, Q = 1 << 20, 1 << 24     # aligned addresses
-ARG = 1
+ARG, SHAPE = 1, 2
 
 
 @pytest.mark.parametrize("change", [dict(h=P, hst=256), dict(h=P, xst=256), dict(h=Q, hst=256, rst=128), dict(h=Q, rst=136)])
@@ -28,3 +30,12 @@ def test_frequencies_beyond_fp32(dims, theta):
 def test_the_largest_frequencies_are_finite():
     turns, _ = B.rope_frequencies([16, 112], 1e-31)
     assert np.isfinite(turns).all() and np.isfinite(turns * np.float32((1 << 24) - 1)).all()
+
+
+@pytest.mark.parametrize("B_,Hq,Sq,status", [(1 << 24, 1, 1, SHAPE), (1 << 10, 1 << 14, 1, SHAPE), (1 << 18, 1, 1 << 13, SHAPE)])
+def test_more_attention_heads_than_a_launch_takes(B_, Hq, Sq, status):
+    """2^24 blocks of 256 threads are one too many for a grid."""
+    from tests.test_oracle_block import _attn_args
+    a = _attn_args(B=B_, Hq=Hq, Hkv=Hq, Sq=Sq, Skv=16, D=8)
+    assert B.attention_workspace_bytes(B_, Sq, 16, Hq, Hq, 8) == 0
+    assert B.lib().svdq_attention(C.byref(a), P, 1 << 40, None) == status
