@@ -1004,8 +1004,9 @@ extern "C" svdq_status svdq_attention(const svdq_attention_args* a, void* ws, si
   const float scale = a->scale < 0.f ? -a->scale : a->scale > 0.f ? a->scale : 1.f;
   p.flip = a->scale < 0.f;
   p.qmul = a->scale < 0.f ? -1.f : a->scale > 0.f ? 1.f : 0.f;
-  p.c1 = scale * log2e;
-  // finite, so that a score of 0 stays 0 under the smallest cap
+  // all finite, so that a score of 0 stays 0 at the largest scale and under the
+  // smallest cap
+  p.c1 = fminf(scale * log2e, 3.0e38f);
   p.c2 = a->softcap > 0.f ? fminf(2.f * scale / a->softcap * log2e, 3.0e38f) : 0.f;
   p.c3 = a->softcap * log2e;
   p.c4 = a->softcap > 0.f ? fminf(scale / a->softcap, 3.0e38f) : 0.f;

@@ -59,3 +59,16 @@ def test_a_large_cap_is_as_good_as_none():
     free = values(_gpu(q, k, v))
     far = values(_gpu(q, k, v, softcap=1e7))        # scores of about 10: tanh(x) = x within 1e-12
     assert np.abs(far - free).max() <= 2 * 2.0**-8 * np.abs(free).max()
+
+
+@pytest.mark.parametrize("Sq,H", [(1, 2), (200, 160)])
+@pytest.mark.parametrize("cap", [0.0, 1.0, 1e6])
+def test_the_largest_scales_leave_scores_of_zero(Sq, H, cap):
+    """Times log2 e they leave fp32; a query of zeros still weighs its keys alike."""
+    D, Skv = 64, 150
+    (_, _), (k, _), (v, vv) = _make(1, Sq, Skv, H, H // 2, D, "bf16", 20)
+    q = torch.zeros((1, Sq, H, D), dtype=torch.bfloat16, device="cuda")
+    want = np.repeat(vv.mean(1), 2, axis=1)[:, None]
+    for scale in (3e38, -3e38, 1e-45):
+        o = values(_gpu(q, k, v, scale=scale, softcap=cap))
+        assert np.abs(o - want).max() <= 2.0**-7 * np.abs(vv).mean(1).max(), scale
