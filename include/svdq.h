@@ -507,6 +507,150 @@ typedef struct svdq_attention_args {
 size_t svdq_attention_workspace_bytes(int32_t B, int32_t Sq, int32_t Skv, int32_t Hq, int32_t Hkv, int32_t D);
 svdq_status svdq_attention(const svdq_attention_args* args, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------- a paged key-value cache ------------------------ */
+
+/* Keys and values of many requests in pages of equal size.  A request's
+ * positions p lie in the pages that its row of a table names: position p in
+ * place p % page of page table[p / page].  Requests may share pages.
+ *   SVDQ_KV_VALUES  16-bit values of the calls' type, stored as they are;
+ *   SVDQ_KV_INT8    codes -127..127, s = max |x| times the fp32 nearest to 1 / 127
+ *                   (0 below 2^-126);
+ *   SVDQ_KV_FP8     E4M3 codes, s the least power of two, at least 2^-126, with
+ *                   max |x| / s <= 448 (0 for zeros),
+ * one fp32 s for the D elements of a token and head, separately for keys and
+ * values; codes are x / s rounded to the nearest, ties to even (exactly: for
+ * INT8 the quotient itself decides, not its fp32 rounding).  A vector that holds
+ * an infinity or a NaN gets s = NaN and codes of 0: all of it reads as NaN. */
+typedef enum svdq_kv_format { SVDQ_KV_VALUES = 0, SVDQ_KV_INT8 = 1, SVDQ_KV_FP8 = 2 } svdq_kv_format;
+
+#define SVDQ_KV_MAX_HEAD_DIM 128
+
+typedef struct svdq_kv_cache {
+  int32_t pages;                /* 1..2^28 */
+  int32_t page;                 /* tokens of a page: 16, 32, 64, 128 or 256 */
+  int32_t heads;                /* K/V heads, 1..65536 */
+  int32_t D;                    /* head dimension: a multiple of 16, 16..SVDQ_KV_MAX_HEAD_DIM */
+  int32_t format;               /* svdq_kv_format */
+  void *k, *v;                  /* device: k [pages][heads][page][D], v [pages][heads][D][page] (each element's
+                                   values of a page side by side, the order in which attention multiplies them) */
+  float *k_scale, *v_scale;     /* device [pages][heads][page]; NULL for SVDQ_KV_VALUES */
+  int64_t k_page, v_page, scale_page;   /* elements from one page to the next: at least heads page D (heads page),
+                                   multiples of 16 bytes; everything inside a page is contiguous */
+} svdq_kv_cache;
+
+typedef struct svdq_cache_write_args {
+  int32_t M;                    /* tokens, 1..2^20; ceil(M / 16) heads < 2^24 */
+  int32_t B, T;                 /* the table: requests and pages of each, B >= 1, 1 <= T, T page <= 2^24 */
+  int32_t dtype;
+  const int32_t* table;         /* device, row b at b * table_row */
+  int64_t table_row;            /* at least T (any if B == 1) */
+  const int32_t* entry;         /* device [M]: the request of a token, or NULL: token m is of request m (M <= B) */
+  const int32_t* position;      /* device [M] */
+  const uint16_t *k, *v;        /* device, element (m, h, d) at m * token + h * head + d; multiples of 8 elements */
+  int64_t k_token, k_head, v_token, v_head;
+} svdq_cache_write_args;
+
+/* Puts the keys and values of M tokens into the cache.  A token whose position
+ * is negative or past the table, whose entry is not in 0..B-1 or whose page is
+ * not in 0..pages-1 is passed over, and nothing else in the cache changes.  Two
+ * tokens of a call must not name the same place.
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; table, entry, position: 4), UNSUPPORTED, DEVICE. */
+svdq_status svdq_cache_write(const svdq_kv_cache* cache, const svdq_cache_write_args* args, void* stream);
+
+typedef struct svdq_cache_read_args {
+  int32_t B, S, T;              /* requests, positions of each (1..2^24), pages of a table row as above;
+                                   B (ceil(S / 64) + 1) heads < 2^24 */
+  int32_t dtype;
+  const int32_t* table;
+  int64_t table_row;
+  const int32_t* kv_len;        /* device [B]: positions in use (clamped to 0..T page) */
+  const int32_t* start;         /* device [B] or NULL (0): the position that goes to row 0 */
+  uint16_t *k, *v;              /* device, element (b, j, h, d) at b * batch + j * token + h * head + d */
+  int64_t k_batch, k_token, k_head, v_batch, v_token, v_head;   /* multiples of 8 elements */
+} svdq_cache_read_args;
+
+/* k[b, j], v[b, j] = what the cache holds at position start[b] + j (codes times
+ * s in fp32, rounded once), the operands of svdq_attention for a chunk of new
+ * tokens.  Rows whose position is negative, not below kv_len[b], or in a page
+ * outside 0..pages-1 stay as they were.
+ * Errors: as svdq_cache_write (kv_len, start: 4 bytes). */
+svdq_status svdq_cache_read(const svdq_kv_cache* cache, const svdq_cache_read_args* args, void* stream);
+
+typedef struct svdq_paged_attention_args {
+  int32_t B, T;                 /* requests and pages of a table row, as above */
+  int32_t Hq;                   /* query heads: Hq % heads == 0, head h reads K/V head h / (Hq / heads); B Hq < 2^24 */
+  int32_t dtype;
+  int32_t window;               /* > 0: only the last `window` keys in use are visible; 0: all */
+  float scale;                  /* of q . k */
+  float softcap;                /* > 0: scores become softcap * tanh(score / softcap); 0: off */
+  const uint16_t* q;            /* device, element (b, h, d) at b * batch + h * head + d; multiples of 8 elements */
+  uint16_t* o;
+  int64_t q_batch, q_head, o_batch, o_head;
+  const int32_t* table;
+  int64_t table_row;
+  const int32_t* kv_len;        /* device [B]: keys in use, the new token's among them (clamped to 0..T page) */
+  const float* slopes;          /* device [Hq] or NULL: adds -slopes[h] * (kv_len[b] - 1 - j) to the score of key j */
+  float* lse;                   /* device [B, Hq] or NULL: log of the sum of exp(score), -infinity where none is seen */
+} svdq_paged_attention_args;
+
+/* O = softmax(scores) V for one new token of each request, at position
+ * kv_len[b] - 1, over the pages of its row.  score = scale q.k, then the cap,
+ * then the distance bias.  Keys in pages outside 0..pages-1 count as hidden, and
+ * a token that sees no key gets zeros.  What the cache holds at hidden places
+ * (infinities and NaN too) does not reach the output; a visible key's NaN makes
+ * its rows NaN, a value's its element.  Scores, the running maximum and
+ * sum and O are fp32.  Codes are widened exactly, and queries then go to the matrix
+ * unit in fp16, scaled by a power of two for each head; weights are rounded to
+ * fp16 (SVDQ_KV_VALUES: to the call's type) for the product with V, not for
+ * their sum.  The same call on the same inputs gives the same bits.
+ * ws: device, 256-byte aligned, svdq_paged_attention_workspace_bytes() bytes, or
+ * NULL if that is 0; its contents before the call do not matter, and calls that
+ * overlap in time need one each.
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; table, kv_len, slopes, lse: 4),
+ * WORKSPACE, UNSUPPORTED, DEVICE. */
+size_t svdq_paged_attention_workspace_bytes(const svdq_kv_cache* cache, int32_t B, int32_t T, int32_t Hq);
+svdq_status svdq_paged_attention(const svdq_kv_cache* cache, const svdq_paged_attention_args* args, void* ws,
+                                 size_t ws_bytes, void* stream);
+
+/* --------------------------- a block's end ----------------------------- */
+
+typedef enum svdq_norm_kind {
+  SVDQ_NORM_NONE = 0,           /* x */
+  SVDQ_NORM_RMS = 1,            /* x / sqrt(mean x^2 + eps) */
+  SVDQ_NORM_LAYER = 2           /* (x - mean x) / sqrt(mean (x - mean x)^2 + eps) */
+} svdq_norm_kind;
+
+typedef struct svdq_gated_norm_args {
+  int32_t M, K;                 /* rows 1..2^20, columns 8..16384, K % 8 == 0 */
+  int32_t E;                    /* rows of gate, scale and shift, 1..2^20 */
+  int32_t dtype;
+  int32_t post, pre;            /* svdq_norm_kind of the block's output and of the sum */
+  float eps, residual_scale;
+  const uint16_t* x;            /* device [M, K]: the block's output */
+  const uint16_t* residual;     /* device [M, K] or NULL */
+  const uint16_t* post_weight;  /* device [K] or NULL (1) */
+  const uint16_t* weight;       /* device [K] or NULL (1) */
+  const uint16_t *gate, *scale, *shift;   /* device [E, K] or NULL (1, 0, 0) */
+  const int32_t* entry;         /* device [M]: the row of gate, scale and shift (clamped to 0..E-1), or NULL: M / E
+                                   rows in a row share one (M % E == 0) */
+  uint16_t *h, *y;              /* device [M, K] or NULL */
+  uint8_t* q;                   /* device [M, K] contiguous, with s, or NULL */
+  float* s;                     /* device [M, ceil(K / 128)] contiguous */
+  int64_t x_row, residual_row, gate_row, scale_row, shift_row, h_row, y_row;   /* multiples of 8 elements, at least K
+                                   (any for a single row) */
+} svdq_gated_norm_args;
+
+/* The end of one block and the start of the next in one pass:
+ *   b = post(x) post_weight;   h = residual_scale residual + gate[e] b;
+ *   y = (pre(h) weight) (1 + scale[e]) + shift[e],
+ * e the row's entry, everything in fp32 from the fp32 h, each output rounded
+ * once; q, s are y's E4M3 codes and scales as svdq_add_rmsnorm_quantize writes
+ * them.  At least one of h, y, q is given.  h may be x or residual and y may be x
+ * or residual, with the same row stride; other overlap is not allowed.  Finite
+ * rows whose squares leave fp32 have their norm.
+ * Errors: ARG, SHAPE, ALIGN (16 bytes; entry, s: 4), UNSUPPORTED, DEVICE. */
+svdq_status svdq_gated_norm(const svdq_gated_norm_args* args, void* stream);
+
 /* ------------------------------ misc ---------------------------------- */
 
 const char* svdq_status_str(svdq_status s);

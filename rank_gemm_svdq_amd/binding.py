@@ -22,6 +22,8 @@ __all__ = [
     "ABI_VERSION", "mfma_rate_probe", "reservoir_select", "smooth_candidates", "search_workspace_bytes", "smooth_search", "SearchOpts", "SearchResult",
     "add_rmsnorm_quantize", "fp8_linear", "fp8_linear_workspace_bytes", "rope_frequencies", "RopePlan", "rope", "attention",
     "attention_workspace", "attention_workspace_bytes", "FP8_BLOCK", "ROPE_MAX_AXES", "ATTENTION_MAX_HEAD_DIM",
+    "KVCache", "cache_write", "cache_read", "paged_attention", "paged_attention_workspace",
+    "paged_attention_workspace_bytes", "gated_norm", "KV_MAX_HEAD_DIM",
 ]
 
 INT4 = 0
@@ -109,8 +111,8 @@ class SearchResult(C.Structure):
                 ("errors", C.c_void_p), ("best_iter", C.c_int32)]
 
 
-# The block operators' argument structures, for callers of lib() (rope() and
-# attention() below fill theirs in C++).
+# The block operators' argument structures, for callers of lib() (rope(),
+# attention() and the others below fill theirs in C++).
 class RopeArgs(C.Structure):
     _fields_ = ([(n, C.c_int32) for n in ("M", "axes", "pairs", "head_dim", "interleaved", "dtype")]
                 + [(n, C.c_void_p) for n in ("positions", "turns", "axis")]
@@ -124,6 +126,42 @@ class AttentionArgs(C.Structure):
                 + [(n, C.c_void_p) for n in "qkvo"]
                 + [(f"{t}_{n}", C.c_int64) for t in "qkvo" for n in ("batch", "token", "head")]
                 + [(n, C.c_void_p) for n in ("slopes", "kv_len", "prefix", "q_doc", "k_doc")])
+
+
+class KVCacheArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("pages", "page", "heads", "D", "format")]
+                + [(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, C.c_int64) for n in ("k_page", "v_page", "scale_page")])
+
+
+class CacheWriteArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("M", "B", "T", "dtype")]
+                + [("table", C.c_void_p), ("table_row", C.c_int64)]
+                + [(n, C.c_void_p) for n in ("entry", "position", "k", "v")]
+                + [(n, C.c_int64) for n in ("k_token", "k_head", "v_token", "v_head")])
+
+
+class CacheReadArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("B", "S", "T", "dtype")]
+                + [("table", C.c_void_p), ("table_row", C.c_int64)]
+                + [(n, C.c_void_p) for n in ("kv_len", "start", "k", "v")]
+                + [(f"{t}_{n}", C.c_int64) for t in "kv" for n in ("batch", "token", "head")])
+
+
+class PagedAttentionArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("B", "T", "Hq", "dtype", "window")]
+                + [("scale", C.c_float), ("softcap", C.c_float), ("q", C.c_void_p), ("o", C.c_void_p)]
+                + [(n, C.c_int64) for n in ("q_batch", "q_head", "o_batch", "o_head")]
+                + [("table", C.c_void_p), ("table_row", C.c_int64)]
+                + [(n, C.c_void_p) for n in ("kv_len", "slopes", "lse")])
+
+
+class GatedNormArgs(C.Structure):
+    _fields_ = ([(n, C.c_int32) for n in ("M", "K", "E", "dtype", "post", "pre")]
+                + [("eps", C.c_float), ("residual_scale", C.c_float)]
+                + [(n, C.c_void_p) for n in ("x", "residual", "post_weight", "weight", "gate", "scale", "shift", "entry",
+                                             "h", "y", "q", "s")]
+                + [(n + "_row", C.c_int64) for n in ("x", "residual", "gate", "scale", "shift", "h", "y")])
 
 
 _lib = None
@@ -180,12 +218,19 @@ def lib():
     L.svdq_attention_workspace_bytes.restype = sz
     L.svdq_attention_workspace_bytes.argtypes = [i32] * 6
     L.svdq_attention.argtypes = [vp, vp, sz, vp]   # svdq_attention_args
+    L.svdq_cache_write.argtypes = [vp, vp, vp]     # svdq_kv_cache, svdq_cache_write_args
+    L.svdq_cache_read.argtypes = [vp, vp, vp]      # svdq_kv_cache, svdq_cache_read_args
+    L.svdq_paged_attention_workspace_bytes.restype = sz
+    L.svdq_paged_attention_workspace_bytes.argtypes = [vp, i32, i32, i32]
+    L.svdq_paged_attention.argtypes = [vp, vp, vp, sz, vp]   # svdq_kv_cache, svdq_paged_attention_args
+    L.svdq_gated_norm.argtypes = [vp, vp]          # svdq_gated_norm_args
     for name in ("svdq_device_check", "svdq_layer_sizes", "svdq_workspace_layout", "svdq_calib_absmax",
                  "svdq_pack_host", "svdq_prepare", "svdq_attach_lora", "svdq_kernel_layout",
                  "svdq_unpack_activations", "svdq_quantize_lora_down", "svdq_gemm_lora_up",
                  "svdq_linear_forward", "svdq_linear_forward_unfused", "svdq_linear_forward_noalloc",
                  "svdq_smooth_search", "svdq_add_rmsnorm_quantize", "svdq_fp8_linear",
-                 "svdq_fp8_linear_shared", "svdq_rope_frequencies", "svdq_rope", "svdq_attention"):
+                 "svdq_fp8_linear_shared", "svdq_rope_frequencies", "svdq_rope", "svdq_attention",
+                 "svdq_cache_write", "svdq_cache_read", "svdq_paged_attention", "svdq_gated_norm"):
         getattr(L, name).restype = C.c_int
     _lib = L
     return L
@@ -567,7 +612,8 @@ def _block():
         L = lib()
         m.bind(SvdqError, *(C.cast(f, C.c_void_p).value
                             for f in (L.svdq_add_rmsnorm_quantize, L.svdq_fp8_linear_shared,
-                                      L.svdq_fp8_linear_workspace_bytes, L.svdq_rope, L.svdq_attention)))
+                                      L.svdq_fp8_linear_workspace_bytes, L.svdq_rope, L.svdq_attention, L.svdq_cache_write,
+                                      L.svdq_cache_read, L.svdq_paged_attention, L.svdq_gated_norm)))
         _blk = m
     return _blk
 
@@ -648,3 +694,87 @@ def attention(q, k, v, o, ws, scale=None, causal=False, softcap=0.0, slopes=None
     if None.  slopes [Hq] float32; kv_len, prefix [B], q_doc [B, Sq], k_doc
     [B, Skv] int32.  The queries are the last Sq of the kv_len keys' positions."""
     (_blk or _block()).attention(q, k, v, o, ws, scale, causal, softcap, slopes, kv_len, prefix, q_doc, k_doc, stream)
+
+
+KV_MAX_HEAD_DIM = 128           # SVDQ_KV_MAX_HEAD_DIM
+
+
+class KVCache:
+    """A paged cache of keys and values in device memory (svdq_kv_cache).
+
+    k [pages, heads, page, D] and v [pages, heads, D, page]: int8 or
+    float8_e4m3fn codes with float32 k_scale, v_scale [pages, heads, page], or
+    bfloat16, float16 or int16 (bf16 bits) values without.  A page's own elements
+    are contiguous; pages may be any distance apart.  page: 16, 32, .. 256; D a
+    multiple of 16 up to 128.  The cache goes on using these tensors' memory."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.handle = (_blk or _block()).kv_cache(k, v, k_scale, v_scale)
+
+    @classmethod
+    def empty(cls, pages, heads, head_dim, page=64, format="int8", device="cuda"):
+        """A new cache; format "int8", "fp8", "bf16" or "fp16"."""
+        torch = _torch()
+        types = {"int8": torch.int8, "fp8": torch.float8_e4m3fn, "bf16": torch.bfloat16, "fp16": torch.float16}
+        if format not in types:
+            raise ValueError(f"unknown cache format {format!r}")
+        new = lambda *s, dtype: torch.zeros(s, dtype=dtype, device=device)
+        scales = [new(pages, heads, page, dtype=torch.float32) for _ in range(2)] if format in ("int8", "fp8") else []
+        return cls(new(pages, heads, page, head_dim, dtype=types[format]),
+                   new(pages, heads, head_dim, page, dtype=types[format]), *scales)
+
+
+def cache_write(cache, table, position, k, v, entry=None, stream=None):
+    """svdq_cache_write: puts token m (k[m], v[m] [heads, D], any token and head
+    strides that are multiples of 8 elements) at position[m] of request
+    entry[m] (m itself if None), whose pages are table[entry[m]].  table [B, T],
+    position, entry [M] int32.  Tokens with a position, entry or page that does not
+    exist are passed over."""
+    (_blk or _block()).cache_write(cache.handle, table, position, k, v, entry, stream)
+
+
+def cache_read(cache, table, kv_len, k, v, start=None, stream=None):
+    """svdq_cache_read: k[b, j], v[b, j] = the cache's keys and values of request b at
+    position start[b] + j (start 0 if None) below kv_len[b]; other rows stay as
+    they were.  k, v [B, S, heads, D], as attention() takes them."""
+    (_blk or _block()).cache_read(cache.handle, table, kv_len, k, v, start, stream)
+
+
+def paged_attention_workspace_bytes(cache, B, T, Hq):
+    c = KVCacheArgs.from_buffer_copy(cache.handle)
+    return lib().svdq_paged_attention_workspace_bytes(C.byref(c), B, T, Hq)
+
+
+def paged_attention_workspace(q, cache, table):
+    """Workspace of paged_attention() for these shapes (to be kept between calls)."""
+    n = paged_attention_workspace_bytes(cache, table.shape[0], table.shape[1], q.shape[1])
+    return _torch().empty(n, dtype=_torch().uint8, device=q.device)
+
+
+def paged_attention(q, cache, table, kv_len, o, ws, scale=None, softcap=0.0, window=0, slopes=None, lse=None,
+                    stream=None):
+    """svdq_paged_attention: o = softmax(scores) v for one new token of each
+    request, q, o [B, Hq, D], over the kv_len[b] keys (its own among them) in
+    the pages table[b]; ws from paged_attention_workspace().  scale: D ** -0.5 if
+    None.  window: only the last so many keys (0: all).  slopes [Hq], lse
+    [B, Hq] float32; table [B, T], kv_len [B] int32."""
+    (_blk or _block()).paged_attention(cache.handle, q, table, kv_len, o, ws, scale, softcap, window, slopes, lse, stream)
+
+
+_NORMS = {"none": 0, "rms": 1, "layer": 2}      # svdq_norm_kind
+
+
+def gated_norm(x, y=None, q=None, s=None, h=None, residual=None, residual_scale=1.0, post="none", post_weight=None,
+               gate=None, pre="rms", weight=None, scale=None, shift=None, entry=None, eps=1e-6, stream=None):
+    """svdq_gated_norm, the end of a block and the start of the next:
+    b = post(x) post_weight; h = residual_scale residual + gate b;
+    y = pre(h) weight (1 + scale) + shift; q, s = y in E4M3 as add_rmsnorm_quantize
+    writes it.  post, pre: "none", "rms" or "layer".  x, residual, h, y [M, K] (rows
+    may be strided); post_weight, weight [K]; gate, scale, shift [E, K] (rows may
+    be strided), entry [M] int32 their row (None: M / E rows in a row share one).
+    Writes those of h, y, (q, s) that are given."""
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError(f"unknown norm {post if post not in _NORMS else pre!r}")
+    (_blk or _block()).gated_norm(x, y, q, s, h, residual, residual_scale, _NORMS[post], post_weight, gate, _NORMS[pre],
+                                  weight, scale, shift, entry, eps, stream)

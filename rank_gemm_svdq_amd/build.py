@@ -30,6 +30,9 @@ UNITS = [
     ("device_fp8.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_rope.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_attention.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_cache.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_paged.hip", [HIPCC] + DEVICE_FLAGS),
+    ("device_gated.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_search.hip", [HIPCC] + DEVICE_FLAGS),
     ("device_probe.hip", [HIPCC] + DEVICE_FLAGS),
 ]

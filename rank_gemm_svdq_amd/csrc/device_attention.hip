@@ -53,7 +53,7 @@
 // scores do not enter it, so the row is NaN.  (2048 tokens, all visible, 8 heads of
 // 128 46 us, with one NaN in V 83, with nothing else in it 1.7 ms.)
 
-#include "device_block.h"
+#include "device_score.h"
 
 namespace svdq {
 namespace {
@@ -92,7 +92,6 @@ __device__ __forceinline__ float half_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Which (entry, K/V head) and which of its row tiles and key parts a block
 // takes.  Blocks are dealt to the 8 XCDs round robin; with a multiple of 8
@@ -117,39 +116,6 @@ __device__ __forceinline__ void group_order(const AttnP& p, int b, int* grp, int
     *rest = b / p.groups;
   }
 }
-
-// Capped score in powers of two of a raw dot product s: cap tanh(x) log2 e with
-// x = s scale / cap, scale > 0, in one of two forms.
-//   by_exp    cap - 2 cap / (e^2x + 1): five instructions, but a difference of two
-//             numbers of the cap's size, so the score is off by up to 2e-7 cap
-//             whatever its own size.
-//   by_series s (scale log2 e) tanh(x) / x, the quotient a polynomial of degree 6
-//             in x^2 (minimax on |x| <= 1, 5.6e-8 relative); beyond, by_exp, whose
-//             error there is 3e-7 of the result.  As exact under a cap of 1e30 as
-//             without one.
-// Caps up to kSmallCap take by_exp: its error is then below 1.3e-5, that of the
-// weight 2^-16, and the 16-bit weights are off by 2^-11 or 2^-8 anyway.
-// The series is slower (2 x 1000 causal queries of 16 heads of 128 36.9 against
-// 34.1 us, 4 x 1024 of 8 heads of 64 30.3 against 26.9; the latter under a cap of
-// 2, where tiles need both, 39.4).
-constexpr float kSmallCap = 64.0f;
-constexpr float kTanh[7] = {1.0f,           -0.33332987f,   0.13326409f, -0.053498708f,
-                            0.020359759f,   -0.0062593391f, 0.0010582646f};
-__device__ __forceinline__ float by_exp(const AttnP& p, float s) {
-  return fmaf(-2.0f * p.c3, __builtin_amdgcn_rcpf(exp2_(s * p.c2) + 1.0f), p.c3);
-}
-__device__ __forceinline__ float by_series(const AttnP& p, float s) {   // |x| <= 1
-  const float x = s * p.c4, u = x * x;
-  float q = p.cap[6];
-#pragma unroll
-  for (int i = 5; i >= 0; --i) q = fmaf(q, u, p.cap[i]);
-  return s * q;
-}
-__device__ __forceinline__ float capped(const AttnP& p, float s) {
-  return p.a.softcap <= kSmallCap || !(fabsf(s * p.c4) <= 1.0f) ? by_exp(p, s) : by_series(p, s);
-}
-
-constexpr float kLow = -3.402823466e38f;
 
 // The end of 32 rows of a wave (lane l: row row0 + l % 32, O^T as the MFMAs
 // leave it, m and l of the whole row): stored as parts or finished.
@@ -998,19 +964,7 @@ extern "C" svdq_status svdq_attention(const svdq_attention_args* a, void* ws, si
   p.R = pl.R;
   p.tiles = pl.tiles;
   p.groups = pl.groups;
-  // A negative scale turns the signs of Q, scale 0 makes Q zero; what remains
-  // is positive, so a hidden score of -infinity stays one when scaled.
-  constexpr float log2e = 1.44269504088896f;
-  const float scale = a->scale < 0.f ? -a->scale : a->scale > 0.f ? a->scale : 1.f;
-  p.flip = a->scale < 0.f;
-  p.qmul = a->scale < 0.f ? -1.f : a->scale > 0.f ? 1.f : 0.f;
-  // all finite, so that a score of 0 stays 0 at the largest scale and under the
-  // smallest cap
-  p.c1 = fminf(scale * log2e, 3.0e38f);
-  p.c2 = a->softcap > 0.f ? fminf(2.f * scale / a->softcap * log2e, 3.0e38f) : 0.f;
-  p.c3 = a->softcap * log2e;
-  p.c4 = a->softcap > 0.f ? fminf(scale / a->softcap, 3.0e38f) : 0.f;
-  for (int i = 0; i < 7; ++i) p.cap[i] = p.c1 * kTanh[i];
+  set_score(&p, a->scale, a->softcap);
   p.part.splits = pl.splits;
   p.part.o = static_cast<float*>(ws);
   p.part.ml = pl.splits > 1

@@ -1,0 +1,581 @@
+// Attention of one new token of each request over a paged cache, 16-bit values or
+// codes: one pass over K and V, split over the cache's length and joined.
+//
+// Rows.  The G query heads that share a K/V head are the rows of one matrix, 16 to a
+// row tile; a block of four waves takes one or two row tiles of one (request, K/V
+// head) over a share of its keys, the waves in turn.
+//
+// A tile of TK keys (64 codes or 32 values), per wave, all operands straight from
+// memory to registers (16x16x32 MFMA; lane l: c = l % 16, u = l / 16):
+//   S^T = K Q^T   A = K.  Row 4 a + i of score tile t is key KPL a + 4 t + i (KPL =
+//                 TK / 4), and the result's lane then holds row c of Q and
+//                 the keys KPL u .. + KPL of the tile in order.
+//   O^T += V^T P  P as it stands, rounded to 16 bits, is the B operand: 8 keys to an
+//                 MFMA.  A = V^T: element 16 d + c of the keys KPL u .. + KPL, 16
+//                 neighbouring bytes of the cache's order [head][D][place].
+// A lane's KPL keys lie in one page (pages are multiples of 16), so a tile may span
+// pages: every lane looks its own page up, one tile ahead.
+//
+// Codes.  INT8 and E4M3 values are exact in fp16.  A query row goes there scaled by
+// a power of two that brings its largest finite element to [1, 2): what falls below
+// fp16's range is under 2^-24 of that.  The key's scale multiplies the score, and the
+// value's scale the weight, as a multiple of a power of two that all the wave's
+// scales so far stay under.
+//
+// Softmax.  A row's maximum is raised when a tile exceeds it by more than kLag
+// (powers of two), which a vote of the wave finds out without exchanges; weights
+// then carry 2^kLift to the middle of their type's range.
+#include "device_kv.h"
+#include "device_score.h"
+
+namespace svdq {
+namespace {
+
+struct PagedPart {          // how the keys are split over blocks
+  int32_t share, splits;    // keys of a block (a multiple of 256), parts at most
+  float* o;                 // [splits][B Hq][DP]: means of the values
+  float* ml;                // [splits][B Hq][2]: maximum (log2) and sum of weights
+};
+
+struct PagedP {
+  svdq_paged_attention_args a;
+  svdq_kv_cache c;
+  int G, rows, shift;       // heads of a K/V head, blocks for its rows, log2 page
+  float qmul, c1, c2, c3, c4;   // see set_score()
+  float cap[7];
+  bool flip;
+  PagedPart part;
+};
+
+constexpr float kLag = 8.0f;
+// fp16 weights between 2^6 and 2^14 at the maximum: the smallest that keeps its bits
+// is 2^-20 of it, 2^-30 with half of them.  bf16: room for 2^20 of the largest values.
+template <int FMT, int DT>
+constexpr float kLift = FMT == SVDQ_KV_VALUES && DT == SVDQ_BF16 ? -20.0f : 6.0f;
+
+// FP16: codes or fp16 values
+template <bool FP16>
+__device__ __forceinline__ b4f mma16(const b4i& a, const b4i& b, const b4f& c) {
+  if constexpr (FP16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(b8h, a), __builtin_bit_cast(b8h, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8bf, a), __builtin_bit_cast(b8bf, b), c, 0, 0, 0);
+}
+
+// 8 codes as fp16
+template <int FMT>
+__device__ __forceinline__ b4i widen_codes(int lo, int hi) {
+  b4i r;
+  if constexpr (FMT == SVDQ_KV_INT8) {
+    // 1024 + (code + 128) by its bits, less 1152
+    const uint32_t x = (uint32_t)lo ^ 0x80808080u, y = (uint32_t)hi ^ 0x80808080u;
+    const uint32_t w[4] = {__builtin_amdgcn_perm(0x64646464u, x, 0x04010400), __builtin_amdgcn_perm(0x64646464u, x, 0x04030402),
+                           __builtin_amdgcn_perm(0x64646464u, y, 0x04010400), __builtin_amdgcn_perm(0x64646464u, y, 0x04030402)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = __builtin_bit_cast(int, __builtin_bit_cast(b2h, w[i]) - (b2h){(_Float16)1152.0f, (_Float16)1152.0f});
+  } else {
+    r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    r[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    r[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+  }
+  return r;
+}
+
+// over the four lanes of a row
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Keys of request b that are visible, [lo, n), and its first part's first key.
+struct Span {
+  int lo, n, first;
+};
+__device__ __forceinline__ Span span_of(const PagedP& p, int b) {
+  Span s;
+  s.n = min(max(p.a.kv_len[b], 0), p.a.T << p.shift);
+  s.lo = p.a.window > 0 ? max(s.n - p.a.window, 0) : 0;
+  s.first = s.lo & ~63;
+  return s;
+}
+
+template <int FMT, int DT, int DP, bool PAD, int RT>
+__global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
+  constexpr bool CODES = FMT != SVDQ_KV_VALUES;
+  constexpr bool FP16 = CODES || DT == SVDQ_FP16;
+  constexpr int ES = CODES ? 1 : 2;
+  constexpr int KPL = 16 / ES, TK = 4 * KPL;     // keys of a lane and of a tile
+  constexpr int NT = TK / 16;                    // score tiles
+  constexpr int NC = DP * ES / 64;               // 16-byte pieces of K a lane reads of a key
+  constexpr int NS = DP / 32;                    // MFMA steps of a score tile
+  constexpr int ND = DP / 16;                    // element tiles of O
+  constexpr int NU = TK / 32;                    // MFMA steps of O
+  constexpr float LIFT = kLift<FMT, DT>;
+  __shared__ float jo[4][16 * RT][DP + 4];
+  __shared__ float jm[4][16 * RT][2];
+  const svdq_paged_attention_args& a = p.a;
+  const svdq_kv_cache& c = p.c;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lc = lane & 15, lu = lane >> 4;
+  const int id = xcd_order(blockIdx.x, gridDim.x);
+  const int sp = id % p.part.splits, rest = id / p.part.splits;
+  const int rb = rest % p.rows, grp = rest / p.rows, h = grp % c.heads, b = grp / c.heads;
+  const Span sn = span_of(p, b);
+  const int begin = sn.first + sp * p.part.share, end = min(sn.n, begin + p.part.share);
+  if (sp > 0 && begin >= end) return;            // no such part
+  const int D = PAD ? c.D : DP;
+
+  // ---- Q as the B operand
+  b4i qf[RT][NS];
+  float rq[RT];                                  // power of two taken out of a row
+  int qh[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    qh[r] = h * p.G + min(rb * 16 * RT + 16 * r + lc, p.G - 1);
+    const uint16_t* qp = a.q + b * a.q_batch + qh[r] * a.q_head;
+    // the elements that meet K's piece of the same step in this lane
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int d = CODES ? 64 * (s / 2) + 16 * lu + 8 * (s % 2) : 32 * s + 8 * lu;
+      qf[r][s] = (b4i){0, 0, 0, 0};
+      if (!PAD || d < D) qf[r][s] = *reinterpret_cast<const b4i*>(qp + d);
+    }
+    rq[r] = 1.f;
+    if constexpr (CODES) {
+      float top = 0.f;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        float x[8];
+        widen8<DT>(qf[r][s], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (fabsf(x[i]) < __builtin_inff()) top = fmaxf(top, fabsf(x[i]));
+      }
+      top = row_max(top);
+      const int e = max((int)(__float_as_uint(top) >> 23), 1) - 127;   // top < 2^(e + 1)
+      rq[r] = top > 0.f ? ldexpf(1.f, e) : 1.f;
+      const float by = (top > 0.f ? ldexpf(1.f, -e) : 1.f) * p.qmul;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        float x[8];
+        widen8<DT>(qf[r][s], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p.qmul != 0.f ? x[i] * by : 0.f;
+        qf[r][s] = narrow8<SVDQ_FP16>(x);
+      }
+    } else if (!(p.qmul > 0.f)) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[r][s][i] = p.flip ? qf[r][s][i] ^ (int)0x80008000 : 0;
+    }
+  }
+  float slope[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) slope[r] = a.slopes ? a.slopes[qh[r]] * 1.44269504f : 0.f;
+
+  float m[RT], l[RT], iv = 0x1p126f;             // iv: 1 / the power of two that V's scales stay under
+  b4f o[RT][ND];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    m[r] = kLow;
+    l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[r][d] = (b4f){0.f, 0.f, 0.f, 0.f};
+  }
+
+  // page of key j of the request: -1 if there is none
+  const int32_t* table = a.table + b * a.table_row;
+  auto page_of = [&](int j) -> int {
+    const int page = table[min(j >> p.shift, a.T - 1)];
+    return (unsigned)page < (unsigned)c.pages ? page : -1;
+  };
+  const int mask = c.page - 1;
+  const int krow = KPL * (lc >> 2) + (lc & 3);   // key of the lane's row of score tile 0
+
+  for (int j0 = begin + TK * wave; j0 < end; j0 += 4 * TK) {
+    // ---- loads
+    const int kj = j0 + KPL * (lc >> 2), vj = j0 + KPL * lu;
+    const int kpage = page_of(kj), vpage = page_of(vj);
+    b4i kw[NT][NC], vw[ND];
+    b4f ks[NT], vs[NT];
+    {
+      const uint8_t* kp = static_cast<const uint8_t*>(c.k) +
+                          ES * (max(kpage, 0) * c.k_page + (((int64_t)h << p.shift) + ((j0 + krow) & mask)) * D) + 16 * lu;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          kw[t][i] = (b4i){0, 0, 0, 0};
+          if (!PAD || 64 * i + 16 * lu < ES * D) kw[t][i] = *reinterpret_cast<const b4i*>(kp + 4 * t * ES * D + 64 * i);
+        }
+      const uint8_t* vp = static_cast<const uint8_t*>(c.v) +
+                          ES * (max(vpage, 0) * c.v_page + (((int64_t)h * D + lc) << p.shift) + (vj & mask));
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        vw[d] = (b4i){0, 0, 0, 0};
+        if (!PAD || 16 * d < D) vw[d] = *reinterpret_cast<const b4i*>(vp + ((size_t)(16 * d * ES) << p.shift));
+      }
+      if constexpr (CODES) {
+        const int64_t at = max(vpage, 0) * c.scale_page + ((int64_t)h << p.shift) + (vj & mask);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          ks[t] = *reinterpret_cast<const b4f*>(c.k_scale + at + 4 * t);
+          vs[t] = *reinterpret_cast<const b4f*>(c.v_scale + at + 4 * t);
+        }
+      }
+    }
+    // keys [lo, hi) of the lane's are visible
+    const int lo = vpage >= 0 ? sn.lo - vj : KPL, hi = vpage >= 0 ? end - vj : 0;
+    const bool cut = __any(lo > 0 || hi < KPL);
+    if (cut) {
+      // what is hidden takes no part, whatever is there
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t keep = 0;
+#pragma unroll
+        for (int k = 0; k < 4 / ES; ++k) {
+          const int x = 4 / ES * i + k;
+          if (x >= lo && x < hi) keep |= (ES == 1 ? 0xFFu : 0xFFFFu) << (8 * ES * k);
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) vw[d][i] &= (int)keep;
+      }
+      if constexpr (CODES) {
+#pragma unroll
+        for (int x = 0; x < KPL; ++x)
+          if (x < lo || x >= hi) vs[x / 4][x % 4] = 0.f;
+      }
+    }
+
+    // ---- scores
+    b4f s[RT][NT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[r][t] = (b4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int st = 0; st < NS; ++st)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        b4i kf;
+        if constexpr (CODES) kf = widen_codes<FMT>(kw[t][st / 2][2 * (st % 2)], kw[t][st / 2][2 * (st % 2) + 1]);
+        else kf = kw[t][st];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r][t] = mma16<FP16>(kf, qf[r][st], s[r][t]);
+      }
+    if constexpr (CODES) {
+      // room for V's scales
+      float big = 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big = fmaxf(big, vs[t][i]);
+      if (__any(big * iv > 1.0f)) {
+        big = row_max(big);
+        const int e = min(max((int)(__float_as_uint(big) >> 23) - 126, -126), 126);   // big < 2^e
+        const float next = ldexpf(1.f, -e), f = next / iv;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int d = 0; d < ND; ++d) o[r][d] *= f;
+        iv = next;
+      }
+    }
+    b4i pf[RT][NU];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      // in powers of two; rounded here and not in the exponent's sum, so that the largest
+      // of enormous scores is the maximum itself
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if constexpr (CODES) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[r][t][i] = s[r][t][i] * ks[t][i] * rq[r];
+        }
+      if (!(a.softcap > 0.f || a.slopes)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[r][t] *= p.c1;
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float x = s[r][t][i];
+            x = a.softcap > 0.f ? capped(p, x) : x * p.c1;
+            if (a.slopes) x = fmaf(-slope[r], (float)(sn.n - 1 - vj - 4 * t - i), x);
+            s[r][t][i] = x;
+          }
+      }
+      if (cut) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (4 * t + i < lo || 4 * t + i >= hi) s[r][t][i] = -__builtin_inff();
+      }
+      float top = s[r][0][0];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, s[r][t][i]);
+      if (__any(top > m[r] + (LIFT + kLag))) {
+        const float up = fmaxf(m[r], row_max(top) - LIFT);
+        const float f = exp2_(m[r] - up);
+        m[r] = up;
+        l[r] *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[r][d] *= f;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = exp2_(s[r][t][i] - m[r]);
+          l[r] += w[i];
+          if constexpr (CODES) w[i] *= vs[t][i] * iv;
+        }
+        // To the product with V the weights go in 16 bits, as the matrix unit takes them
+        pf[r][t / 2][2 * (t % 2)] = (int)narrow2<FP16 ? SVDQ_FP16 : SVDQ_BF16>(w[0], w[1]);
+        pf[r][t / 2][2 * (t % 2) + 1] = (int)narrow2<FP16 ? SVDQ_FP16 : SVDQ_BF16>(w[2], w[3]);
+      }
+    }
+    // ---- values
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        b4i vf;
+        if constexpr (CODES) vf = widen_codes<FMT>(vw[d][2 * u], vw[d][2 * u + 1]);
+        else vf = vw[d];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) o[r][d] = mma16<FP16>(vf, pf[r][u], o[r][d]);
+      }
+  }
+
+  // ---- join the waves: means and (maximum, sum) through LDS
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const float sum = row_sum(l[r]);
+    // a mean of codes is at most 448, so the scale comes back after the division
+    const float by = sum != 0.f ? 1.0f / sum : 0.f, back = CODES ? 1.0f / iv : 1.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+      *reinterpret_cast<b4f*>(&jo[wave][16 * r + lc][16 * d + 4 * lu]) =
+          (b4f){o[r][d][0] * by * back, o[r][d][1] * by * back, o[r][d][2] * by * back, o[r][d][3] * by * back};
+    if (lu == 0) {
+      jm[wave][16 * r + lc][0] = m[r];
+      jm[wave][16 * r + lc][1] = sum;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * RT * (DP / 4); i += 256) {
+    const int r = i / (DP / 4), d = 4 * (i % (DP / 4)), row = rb * 16 * RT + r;
+    if (row >= p.G || d >= D) continue;
+    float up = jm[0][r][0], sum = 0.f;
+#pragma unroll
+    for (int w = 1; w < 4; ++w) up = fmaxf(up, jm[w][r][0]);
+    b4f x = (b4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = jm[w][r][1] * exp2_(jm[w][r][0] - up);
+      sum += f;
+      x += *reinterpret_cast<const b4f*>(&jo[w][r][d]) * f;
+    }
+    x *= sum != 0.f ? 1.0f / sum : 0.f;
+    const size_t at = (size_t)b * a.Hq + h * p.G + row;
+    if (p.part.splits > 1) {
+      const size_t pt = (size_t)sp * ((size_t)a.B * a.Hq) + at;
+      *reinterpret_cast<b4f*>(p.part.o + pt * DP + d) = x;
+      if (d == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * pt) = make_float2(up, sum);
+    } else {
+      *reinterpret_cast<uint2*>(a.o + b * a.o_batch + (h * p.G + row) * a.o_head + d) =
+          make_uint2(narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]));
+      if (d == 0 && a.lse) a.lse[at] = sum != 0.f ? (up + __log2f(sum)) * 0.693147181f : -__builtin_inff();
+    }
+  }
+}
+
+// Joins the parts of the rows: DP / 8 lanes hold a row's 8-element pieces, and
+// `across` such lane sets (1, 2, .. 16) of a block share the row's parts.
+template <int DT, int DP>
+__global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
+  const svdq_paged_attention_args& a = p.a;
+  constexpr int LPR = DP / 8;
+  __shared__ float part[256][11];   // 8 sums, maximum, sum of weights; 11: odd stride
+  const size_t rows = (size_t)a.B * a.Hq;
+  const int set = threadIdx.x / LPR, g = set % across, d = 8 * (threadIdx.x % LPR);
+  const size_t at = (size_t)blockIdx.x * (256 / LPR / across) + set / across;
+  const bool live = at < rows;
+  float top = kLow, sum = 0.f, o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  if (live) {
+    const Span sn = span_of(p, (int)(at / a.Hq));
+    const int parts = min(p.part.splits, max(1, (sn.n - sn.first + p.part.share - 1) / p.part.share));
+    for (int s = g; s < parts; s += across) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part.ml + 2 * (s * rows + at));
+      const float* op = p.part.o + (s * rows + at) * DP + d;
+      b4f x = (b4f){0.f, 0.f, 0.f, 0.f}, y = x;
+      if (d < p.c.D) {
+        x = *reinterpret_cast<const b4f*>(op);
+        y = *reinterpret_cast<const b4f*>(op + 4);
+      }
+      const float up = fmaxf(top, ml.x), f0 = exp2_(top - up), f = ml.y * exp2_(ml.x - up);
+      sum = fmaf(sum, f0, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i] = fmaf(f, x[i], o[i] * f0);
+        o[4 + i] = fmaf(f, y[i], o[4 + i] * f0);
+      }
+      top = up;
+    }
+  }
+  if (across > 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = o[i];
+    part[threadIdx.x][8] = top;
+    part[threadIdx.x][9] = sum;
+    __syncthreads();
+    if (g == 0) {
+      for (int k = 1; k < across; ++k) {
+        const float* x = part[threadIdx.x + k * LPR];
+        const float up = fmaxf(top, x[8]), f0 = exp2_(top - up), f = exp2_(x[8] - up);
+        sum = fmaf(f, x[9], sum * f0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(f, x[i], o[i] * f0);
+        top = up;
+      }
+    }
+  }
+  if (!live || g != 0 || d >= p.c.D) return;
+  const float by = sum != 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] *= by;
+  const int b = (int)(at / a.Hq), hq = (int)(at % a.Hq);
+  *reinterpret_cast<b4i*>(a.o + b * a.o_batch + hq * a.o_head + d) = narrow8<DT>(o);
+  if (d == 0 && a.lse) a.lse[at] = sum != 0.f ? (top + __log2f(sum)) * 0.693147181f : -__builtin_inff();
+}
+
+int padded_dim(int32_t D) { return D <= 64 ? 64 : 128; }
+
+// The arrangement of a call.  keys: at most so many of a request are visible.
+struct PagedPlan {
+  int G, rows, share, splits;
+};
+PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
+  PagedPlan p;
+  p.G = Hq / c.heads;
+  p.rows = p.G <= 16 ? 1 : (p.G + 31) / 32;
+  const int64_t blocks = (int64_t)B * c.heads * p.rows;
+  // Blocks that the chip holds twice over, as lengths differ, and at least 1024 keys
+  // each: shorter parts cost more in their start and end, and in the join.
+  const int64_t want = (4 * kCus + blocks - 1) / blocks;
+  int64_t share = ((keys + want - 1) / want + 255) / 256 * 256;
+  if (share < 1024) share = 1024;
+  p.share = (int)share;
+  p.splits = (int)((keys + share - 1) / share);
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+size_t plan_bytes(const PagedPlan& p, int32_t B, int32_t Hq, int32_t D) {
+  if (p.splits == 1) return 0;
+  const size_t rows = (size_t)B * Hq;
+  return align256(p.splits * rows * padded_dim(D) * 4) + align256(p.splits * rows * 8);
+}
+
+template <int FMT, int DT, int DP, bool PAD>
+svdq_status launch_rows(const PagedP& p, const PagedPlan& pl, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)p.a.B * p.c.heads * pl.rows * pl.splits));
+  if (pl.G <= 16) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1>), grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 2>), grid, dim3(256), 0, st, p);
+  svdq_status s = launched();
+  if (s == SVDQ_OK && pl.splits > 1) {
+    int across = 1;
+    while (across < 16 && across < pl.splits) across *= 2;
+    const int per = 256 / (DP / 8) / across;
+    const size_t rows = (size_t)p.a.B * p.a.Hq;
+    hipLaunchKernelGGL((paged_join<DT, DP>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, p, across);
+    s = launched();
+  }
+  return s;
+}
+template <int FMT, int DT>
+svdq_status launch_dim(const PagedP& p, const PagedPlan& pl, hipStream_t st) {
+  if (p.c.D == 128) return launch_rows<FMT, DT, 128, false>(p, pl, st);
+  if (p.c.D > 64) return launch_rows<FMT, DT, 128, true>(p, pl, st);
+  if (p.c.D == 64) return launch_rows<FMT, DT, 64, false>(p, pl, st);
+  return launch_rows<FMT, DT, 64, true>(p, pl, st);
+}
+template <int FMT>
+svdq_status launch_type(const PagedP& p, const PagedPlan& pl, hipStream_t st) {
+  return p.a.dtype == SVDQ_BF16 ? launch_dim<FMT, SVDQ_BF16>(p, pl, st) : launch_dim<FMT, SVDQ_FP16>(p, pl, st);
+}
+
+bool sizes_fit(const svdq_kv_cache& c, int32_t B, int32_t T, int32_t Hq) {
+  return B >= 1 && T >= 1 && (int64_t)T * c.page <= (1 << 24) && Hq >= 1 && Hq <= 65536 && Hq % c.heads == 0 &&
+         (int64_t)B * Hq < (1 << 24);
+}
+
+}  // namespace
+}  // namespace svdq
+
+using namespace svdq;
+
+extern "C" size_t svdq_paged_attention_workspace_bytes(const svdq_kv_cache* cache, int32_t B, int32_t T, int32_t Hq) {
+  if (!cache || cache_sizes(*cache) != SVDQ_OK || !sizes_fit(*cache, B, T, Hq)) return 0;
+  return plan_bytes(plan_of(*cache, B, (int64_t)T * cache->page, Hq), B, Hq, cache->D);
+}
+
+extern "C" svdq_status svdq_paged_attention(const svdq_kv_cache* cache, const svdq_paged_attention_args* a, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  if (!cache || !a || !a->q || !a->o || !a->table || !a->kv_len) return SVDQ_ERR_ARG;
+  svdq_status s = cache_check(*cache);
+  if (s != SVDQ_OK) return s;
+  if (!is_dtype(a->dtype)) return SVDQ_ERR_UNSUPPORTED;
+  if (!sizes_fit(*cache, a->B, a->T, a->Hq) || (a->B > 1 && a->table_row < a->T)) return SVDQ_ERR_SHAPE;
+  const float big = 3.0e38f;
+  if (!(a->scale >= -big && a->scale <= big) || !(a->softcap >= 0.f && a->softcap <= big) || a->window < 0)
+    return SVDQ_ERR_ARG;
+  for (int64_t st : {a->q_batch, a->q_head, a->o_batch, a->o_head})
+    if (st % 8 != 0) return SVDQ_ERR_ALIGN;
+  if (!on16(a->q) || !on16(a->o) || !on4(a->table) || !on4(a->kv_len) || !on4(a->slopes) || !on4(a->lse))
+    return SVDQ_ERR_ALIGN;
+  const int64_t all = (int64_t)a->T * cache->page;
+  // a window starts inside a tile: up to 63 keys before it are passed over
+  const int64_t near = (int64_t)a->window + 63, keys = a->window > 0 && near < all ? near : all;
+  PagedPlan pl = plan_of(*cache, a->B, keys, a->Hq);
+  // the workspace is asked for without the window: no more parts than without it
+  const PagedPlan whole = plan_of(*cache, a->B, all, a->Hq);
+  if (pl.splits > whole.splits) pl = whole;
+  const size_t need = plan_bytes(pl, a->B, a->Hq, cache->D);
+  if (need > 0 && (!ws || ws_bytes < need)) return !ws ? SVDQ_ERR_ARG : SVDQ_ERR_WORKSPACE;
+  if (((uintptr_t)ws & 255u) != 0) return SVDQ_ERR_ALIGN;
+  if ((s = device_ok()) != SVDQ_OK) return s;
+  PagedP p;
+  p.a = *a;
+  p.c = *cache;
+  if (a->B == 1) p.a.table_row = 0;
+  p.G = pl.G;
+  p.rows = pl.rows;
+  p.shift = __builtin_ctz(cache->page);
+  set_score(&p, a->scale, a->softcap);
+  p.part.share = pl.share;
+  p.part.splits = pl.splits;
+  p.part.o = static_cast<float*>(ws);
+  p.part.ml = pl.splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                                       align256((size_t)pl.splits * a->B * a->Hq * padded_dim(cache->D) * 4))
+                            : nullptr;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (cache->format == SVDQ_KV_INT8) return launch_type<SVDQ_KV_INT8>(p, pl, st);
+  if (cache->format == SVDQ_KV_FP8) return launch_type<SVDQ_KV_FP8>(p, pl, st);
+  return launch_type<SVDQ_KV_VALUES>(p, pl, st);
+}

@@ -17,6 +17,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <string>
 
 #include "../../include/svdq.h"
@@ -29,6 +30,10 @@ decltype(&svdq_fp8_linear_shared) g_linear = nullptr;
 decltype(&svdq_fp8_linear_workspace_bytes) g_linear_bytes = nullptr;
 decltype(&svdq_rope) g_rope = nullptr;
 decltype(&svdq_attention) g_attention = nullptr;
+decltype(&svdq_cache_write) g_cache_write = nullptr;
+decltype(&svdq_cache_read) g_cache_read = nullptr;
+decltype(&svdq_paged_attention) g_paged = nullptr;
+decltype(&svdq_gated_norm) g_gated = nullptr;
 
 // thrown inside a call once the Python error is set
 struct Refused {};
@@ -359,15 +364,225 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (SvdqError, addresses of svdq_add_rmsnorm_quantize, svdq_fp8_linear_shared, svdq_fp8_linear_workspace_bytes,
-// svdq_rope, svdq_attention)
+// A paged cache as KVCache hands it over: packed once, its tensors checked then.
+struct Pages {
+  svdq_kv_cache c;
+  int32_t dev;
+  int32_t type;   // svdq_dtype of stored values, -1: codes
+};
+
+// (k, v, k_scale, v_scale) -> bytes of a Pages
+PyObject* kv_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const char* where = "KVCache";
+  Pages p{};
+  PyObject* none = guarded(where, n, 4, [&] {
+    Call c{where};
+    const at::Tensor &k = c.tensor(a[0], "k"), &v = c.tensor(a[1], "v");
+    if (!k.is_cuda()) refuse(SVDQ_ERR_ARG, where, "k is not in GPU memory");
+    p.dev = c.dev = k.get_device();
+    const at::ScalarType type = k.scalar_type();
+    p.type = -1;
+    if (type == at::kChar) {
+      p.c.format = SVDQ_KV_INT8;
+    } else if (type == at::kFloat8_e4m3fn) {
+      p.c.format = SVDQ_KV_FP8;
+    } else if (type == at::kBFloat16 || type == at::kShort || type == at::kHalf) {
+      p.c.format = SVDQ_KV_VALUES;
+      p.type = type == at::kHalf ? SVDQ_FP16 : SVDQ_BF16;
+    } else {
+      refuse(SVDQ_ERR_ARG, where, "k has dtype %s, expected int8, float8_e4m3fn, bfloat16, float16 or int16 (bf16 bits)",
+             c10::toString(type));
+    }
+    if (k.dim() != 4) refuse(SVDQ_ERR_SHAPE, where, "k has shape %s, expected (pages, heads, page, D)", shape_text(k.sizes()).c_str());
+    const int64_t pages = k.size(0), heads = k.size(1), page = k.size(2), D = k.size(3);
+    p.c.pages = small(c, "pages", pages);
+    p.c.heads = small(c, "heads", heads);
+    p.c.page = small(c, "page", page);
+    p.c.D = small(c, "D", D);
+    // whole pages, any distance apart
+    auto pages_of = [&](PyObject* o, const char* what, at::ScalarType t, at::IntArrayRef shape, int64_t* step) -> void* {
+      const at::Tensor& x = c.tensor(o, what);
+      c.here(x, what);
+      c.of(x, what, t);
+      c.shaped(x, what, shape);
+      int64_t size = 1;
+      for (int64_t d = (int64_t)shape.size() - 1; d > 0; size *= shape[d--])
+        if (shape[d] > 1 && x.stride(d) != size) refuse(SVDQ_ERR_ARG, where, "the pages of %s are not contiguous", what);
+      *step = pages > 1 ? x.stride(0) : size;
+      return x.data_ptr();
+    };
+    p.c.k = pages_of(a[0], "k", type, {pages, heads, page, D}, &p.c.k_page);
+    p.c.v = pages_of(a[1], "v", type, {pages, heads, D, page}, &p.c.v_page);
+    const bool scaled = p.type < 0;
+    if (scaled != (a[2] != Py_None) || scaled != (a[3] != Py_None))
+      refuse(SVDQ_ERR_ARG, where, "codes have k_scale and v_scale, values none");
+    if (scaled) {
+      int64_t other = 0;
+      p.c.k_scale = static_cast<float*>(pages_of(a[2], "k_scale", at::kFloat, {pages, heads, page}, &p.c.scale_page));
+      p.c.v_scale = static_cast<float*>(pages_of(a[3], "v_scale", at::kFloat, {pages, heads, page}, &other));
+      if (other != p.c.scale_page) refuse(SVDQ_ERR_ARG, where, "k_scale and v_scale have different strides");
+    }
+  });
+  if (!none) return nullptr;
+  Py_DECREF(none);
+  return PyBytes_FromStringAndSize(reinterpret_cast<const char*>(&p), sizeof p);
+}
+
+// the cache of a call whose first tensor is known
+Pages pages(const Call& c, PyObject* o) {
+  if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != (Py_ssize_t)sizeof(Pages))
+    refuse(SVDQ_ERR_ARG, c.where, "not a KVCache");
+  Pages p;
+  std::memcpy(&p, PyBytes_AS_STRING(o), sizeof p);
+  if (p.dev != c.dev) refuse(SVDQ_ERR_ARG, c.where, "the cache is on cuda:%d, expected cuda:%d", (int)p.dev, c.dev);
+  if (p.type >= 0 && p.type != c.dtype) refuse(SVDQ_ERR_ARG, c.where, "the cache holds values of another type");
+  return p;
+}
+
+// a table of pages [B, T], rows any distance apart
+const int32_t* table(const Call& c, PyObject* o, int32_t* B, int32_t* T, int64_t* row) {
+  const at::Tensor& t = c.tensor(o, "table");
+  c.here(t, "table");
+  c.of(t, "table", at::kInt);
+  if (t.dim() != 2) refuse(SVDQ_ERR_SHAPE, c.where, "table has shape %s, expected (B, T)", shape_text(t.sizes()).c_str());
+  if (t.size(1) > 1 && t.stride(1) != 1) refuse(SVDQ_ERR_ARG, c.where, "the rows of table are not contiguous");
+  *B = small(c, "B", t.size(0));
+  *T = small(c, "T", t.size(1));
+  *row = t.size(0) > 1 ? t.stride(0) : t.size(1);
+  return static_cast<int32_t*>(t.data_ptr());
+}
+
+// (cache, table, position, k, v, entry, stream)
+PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const char* where = "svdq_cache_write";
+  return guarded(where, n, 7, [&] {
+    Call c{where};
+    const at::Tensor &k = c.first(a[3], "k", 3), &v = c.tensor(a[4], "v");
+    const Pages p = pages(c, a[0]);
+    svdq_cache_write_args w{};
+    w.M = small(c, "M", k.size(0));
+    w.dtype = c.dtype;
+    w.table = table(c, a[1], &w.B, &w.T, &w.table_row);
+    w.k = c.values(k, "k", {w.M, p.c.heads, p.c.D});
+    w.v = c.values(v, "v", {w.M, p.c.heads, p.c.D});
+    w.k_token = step(k, 0), w.k_head = step(k, 1), w.v_token = step(v, 0), w.v_head = step(v, 1);
+    w.position = static_cast<int32_t*>(c.plain(a[2], "position", at::kInt, {w.M}));
+    w.entry = static_cast<int32_t*>(c.optional(a[5], "entry", at::kInt, {w.M}));
+    void* st = c.stream(a[6]);
+    c.done(without_gil([&] { return g_cache_write(&p.c, &w, st); }));
+  });
+}
+
+// (cache, table, kv_len, k, v, start, stream)
+PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const char* where = "svdq_cache_read";
+  return guarded(where, n, 7, [&] {
+    Call c{where};
+    const at::Tensor &k = c.first(a[3], "k", 4), &v = c.tensor(a[4], "v");
+    const Pages p = pages(c, a[0]);
+    svdq_cache_read_args r{};
+    r.dtype = c.dtype;
+    r.table = table(c, a[1], &r.B, &r.T, &r.table_row);
+    r.S = small(c, "S", k.size(1));
+    r.k = c.values(k, "k", {r.B, r.S, p.c.heads, p.c.D});
+    r.v = c.values(v, "v", {r.B, r.S, p.c.heads, p.c.D});
+    r.k_batch = step(k, 0), r.k_token = step(k, 1), r.k_head = step(k, 2);
+    r.v_batch = step(v, 0), r.v_token = step(v, 1), r.v_head = step(v, 2);
+    r.kv_len = static_cast<int32_t*>(c.plain(a[2], "kv_len", at::kInt, {r.B}));
+    r.start = static_cast<int32_t*>(c.optional(a[5], "start", at::kInt, {r.B}));
+    void* st = c.stream(a[6]);
+    c.done(without_gil([&] { return g_cache_read(&p.c, &r, st); }));
+  });
+}
+
+// (cache, q, table, kv_len, o, ws, scale, softcap, window, slopes, lse, stream)
+PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const char* where = "svdq_paged_attention";
+  return guarded(where, n, 12, [&] {
+    Call c{where};
+    const at::Tensor &q = c.first(a[1], "q", 3), &o = c.tensor(a[4], "o");
+    const Pages pg = pages(c, a[0]);
+    svdq_paged_attention_args p{};
+    p.table = table(c, a[2], &p.B, &p.T, &p.table_row);
+    p.Hq = small(c, "Hq", q.size(1));
+    p.dtype = c.dtype;
+    const int64_t window = PyLong_AsLongLong(a[8]);
+    if (window == -1 && PyErr_Occurred()) throw Refused();
+    if (window < 0 || window > INT32_MAX) refuse(SVDQ_ERR_ARG, where, "window is %lld", (long long)window);
+    p.window = (int32_t)window;
+    p.scale = a[6] == Py_None ? (float)(1.0 / std::sqrt((double)pg.c.D)) : (float)number(a[6]);
+    p.softcap = (float)number(a[7]);
+    p.q = c.values(q, "q", {p.B, p.Hq, pg.c.D});
+    p.o = c.values(o, "o", {p.B, p.Hq, pg.c.D});
+    p.q_batch = step(q, 0), p.q_head = step(q, 1), p.o_batch = step(o, 0), p.o_head = step(o, 1);
+    p.kv_len = static_cast<int32_t*>(c.plain(a[3], "kv_len", at::kInt, {p.B}));
+    p.slopes = static_cast<float*>(c.optional(a[9], "slopes", at::kFloat, {p.Hq}));
+    p.lse = static_cast<float*>(c.optional(a[10], "lse", at::kFloat, {p.B, p.Hq}));
+    size_t bytes = 0;
+    void *ws = c.memory(a[5], &bytes), *st = c.stream(a[11]);
+    c.done(without_gil([&] { return g_paged(&pg.c, &p, ws, bytes, st); }));
+  });
+}
+
+// (x, y, q, s, h, residual, residual_scale, post, post_weight, gate, pre, weight, scale, shift, entry, eps, stream)
+PyObject* gated_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  const char* where = "svdq_gated_norm";
+  return guarded(where, n, 17, [&] {
+    Call c{where};
+    const at::Tensor& x = c.first(a[0], "x", 2);
+    svdq_gated_norm_args p{};
+    p.M = small(c, "M", x.size(0));
+    p.K = small(c, "K", x.size(1));
+    p.E = 1;
+    p.dtype = c.dtype;
+    p.post = small(c, "post", PyLong_AsLongLong(a[7]));
+    p.pre = small(c, "pre", PyLong_AsLongLong(a[10]));
+    p.residual_scale = (float)number(a[6]);
+    p.eps = (float)number(a[15]);
+    auto rows = [&](PyObject* o, const char* what, int64_t count, int64_t* st) -> uint16_t* {
+      if (o == Py_None) return nullptr;
+      const at::Tensor& t = c.tensor(o, what);
+      uint16_t* at = c.values(t, what, {count, p.K});
+      *st = count > 1 ? t.stride(0) : p.K;
+      return at;
+    };
+    for (int i : {9, 12, 13})
+      if (a[i] != Py_None) {
+        const at::Tensor& t = c.tensor(a[i], i == 9 ? "gate" : i == 12 ? "scale" : "shift");
+        if (t.dim() == 2) p.E = small(c, "E", t.size(0));   // of the first; the others have to agree
+        break;
+      }
+    p.x = rows(a[0], "x", p.M, &p.x_row);
+    p.y = rows(a[1], "y", p.M, &p.y_row);
+    p.h = rows(a[4], "h", p.M, &p.h_row);
+    p.residual = rows(a[5], "residual", p.M, &p.residual_row);
+    p.gate = rows(a[9], "gate", p.E, &p.gate_row);
+    p.scale = rows(a[12], "scale", p.E, &p.scale_row);
+    p.shift = rows(a[13], "shift", p.E, &p.shift_row);
+    p.post_weight = static_cast<uint16_t*>(c.optional(a[8], "post_weight", c.own, {p.K}));
+    p.weight = static_cast<uint16_t*>(c.optional(a[11], "weight", c.own, {p.K}));
+    p.entry = static_cast<int32_t*>(c.optional(a[14], "entry", at::kInt, {p.M}));
+    if ((a[2] == Py_None) != (a[3] == Py_None)) refuse(SVDQ_ERR_ARG, where, "q and s go together");
+    if (a[2] != Py_None) {
+      const at::Tensor& q = c.tensor(a[2], "q");
+      p.q = c.codes(q, "q");
+      c.shaped(q, "q", {p.M, p.K});
+      p.s = static_cast<float*>(c.plain(a[3], "s", at::kFloat, {p.M, (p.K + SVDQ_FP8_BLOCK - 1) / SVDQ_FP8_BLOCK}));
+    }
+    void* st = c.stream(a[16]);
+    c.done(without_gil([&] { return g_gated(&p, st); }));
+  });
+}
+
+// (SvdqError, addresses of the functions below in their order)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind: an exception type and five addresses");
+  constexpr int kAddresses = 9;
+  if (n != 1 + kAddresses) {
+    PyErr_Format(PyExc_TypeError, "bind: an exception type and %d addresses", kAddresses);
     return nullptr;
   }
-  void* at[5];
-  for (int i = 0; i < 5; ++i) {
+  void* at[kAddresses];
+  for (int i = 0; i < kAddresses; ++i) {
     at[i] = PyLong_AsVoidPtr(a[i + 1]);
     if (!at[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: a null address");
@@ -379,6 +594,10 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_linear_bytes = reinterpret_cast<decltype(g_linear_bytes)>(at[2]);
   g_rope = reinterpret_cast<decltype(g_rope)>(at[3]);
   g_attention = reinterpret_cast<decltype(g_attention)>(at[4]);
+  g_cache_write = reinterpret_cast<decltype(g_cache_write)>(at[5]);
+  g_cache_read = reinterpret_cast<decltype(g_cache_read)>(at[6]);
+  g_paged = reinterpret_cast<decltype(g_paged)>(at[7]);
+  g_gated = reinterpret_cast<decltype(g_gated)>(at[8]);
   Py_INCREF(a[0]);
   Py_XSETREF(g_error, a[0]);
   Py_RETURN_NONE;
@@ -386,6 +605,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(bind), FAST(add_rmsnorm_quantize), FAST(fp8_linear), FAST(rope), FAST(attention),
+                         FAST(kv_cache), FAST(cache_write), FAST(cache_read), FAST(paged_attention), FAST(gated_norm),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", "argument marshalling of the block operators", -1, methods,
