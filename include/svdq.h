@@ -598,11 +598,13 @@ typedef struct svdq_paged_attention_args {
  * then the distance bias.  Keys in pages outside 0..pages-1 count as hidden, and
  * a token that sees no key gets zeros.  What the cache holds at hidden places
  * (infinities and NaN too) does not reach the output; a visible key's NaN makes
- * its rows NaN, a value's its element.  Scores, the running maximum and
- * sum and O are fp32.  Codes are widened exactly, and queries then go to the matrix
- * unit in fp16, scaled by a power of two for each head; weights are rounded to
- * fp16 (SVDQ_KV_VALUES: to the call's type) for the product with V, not for
- * their sum.  The same call on the same inputs gives the same bits.
+ * its rows NaN, a value's its element (all of them where its s is NaN).  Scores, the
+ * running maximum and sum and O are fp32.  For the matrix unit queries are rounded to
+ * 16 bits of their row's largest magnitude (SVDQ_KV_INT8) or to fp16 scaled by a power
+ * of two (SVDQ_KV_FP8); with either a query that holds an infinity or a NaN gets NaN
+ * where it sees a key.  Weights are rounded to fp16 (SVDQ_KV_VALUES: to the call's
+ * type) for the product with V, not for their sum.  The same call on the same inputs
+ * gives the same bits.
  * ws: device, 256-byte aligned, svdq_paged_attention_workspace_bytes() bytes, or
  * NULL if that is 0; its contents before the call do not matter, and calls that
  * overlap in time need one each.

@@ -14,13 +14,15 @@
 //                 MFMA.  A = V^T: element 16 d + c of the keys KPL u .. + KPL, 16
 //                 neighbouring bytes of the cache's order [head][D][place].
 // A lane's KPL keys lie in one page (pages are multiples of 16), so a tile may span
-// pages: every lane looks its own page up, one tile ahead.
+// pages: every lane looks its own page up, two tiles ahead.  A tile's operands are asked
+// for as soon as the registers that they go to have been used for the tile before.
 //
-// Codes.  INT8 and E4M3 values are exact in fp16.  A query row goes there scaled by
-// a power of two that brings its largest finite element to [1, 2): what falls below
-// fp16's range is under 2^-24 of that.  The key's scale multiplies the score, and the
-// value's scale the weight, as a multiple of a power of two that all the wave's
-// scales so far stay under.
+// Codes.  E4M3 goes to fp16, exactly, and a query row with it, scaled by a power of two
+// that brings its largest element to [1, 2): what falls below fp16's range is under
+// 2^-24 of that.  INT8 keys are multiplied as they are by queries of 16 bits in two parts
+// of 8, summed exactly in int32; INT8 values become fp16 of their bits (widen_codes).
+// The key's scale multiplies the score, and the value's scale the weight, as a multiple
+// of a power of two that all the wave's scales so far stay under.
 //
 // Softmax.  A row's maximum is raised when a tile exceeds it by more than kLag
 // (powers of two), which a vote of the wave finds out without exchanges; weights
@@ -41,6 +43,7 @@ struct PagedP {
   svdq_paged_attention_args a;
   svdq_kv_cache c;
   int G, rows, shift;       // heads of a K/V head, blocks for its rows, log2 page
+  uint32_t by_splits, by_heads;   // 2^32 / parts and / heads, rounded up (0: does not serve)
   float qmul, c1, c2, c3, c4;   // see set_score()
   float cap[7];
   bool flip;
@@ -62,18 +65,18 @@ __device__ __forceinline__ b4f mma16(const b4i& a, const b4i& b, const b4f& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8bf, a), __builtin_bit_cast(b8bf, b), c, 0, 0, 0);
 }
 
-// 8 codes as fp16
+// 8 codes as fp16.  E4M3: as they are, in order.  INT8: (code + 128) 2^-24, fp16
+// values below its normal range, in the order 0, 2, 1, 3, 4, 6, 5, 7: the bytes
+// need no arithmetic, and the 128 is taken out of the sums at the end.
 template <int FMT>
 __device__ __forceinline__ b4i widen_codes(int lo, int hi) {
   b4i r;
   if constexpr (FMT == SVDQ_KV_INT8) {
-    // 1024 + (code + 128) by its bits, less 1152
     const uint32_t x = (uint32_t)lo ^ 0x80808080u, y = (uint32_t)hi ^ 0x80808080u;
-    const uint32_t w[4] = {__builtin_amdgcn_perm(0x64646464u, x, 0x04010400), __builtin_amdgcn_perm(0x64646464u, x, 0x04030402),
-                           __builtin_amdgcn_perm(0x64646464u, y, 0x04010400), __builtin_amdgcn_perm(0x64646464u, y, 0x04030402)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = __builtin_bit_cast(int, __builtin_bit_cast(b2h, w[i]) - (b2h){(_Float16)1152.0f, (_Float16)1152.0f});
+    r[0] = (int)(x & 0x00FF00FFu);
+    r[1] = (int)__builtin_amdgcn_perm(0, x, 0x0C030C01);
+    r[2] = (int)(y & 0x00FF00FFu);
+    r[3] = (int)__builtin_amdgcn_perm(0, y, 0x0C030C01);
   } else {
     r[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
     r[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
@@ -93,6 +96,14 @@ __device__ __forceinline__ float row_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// The kernel's arguments, read again where they are used: what only the rare paths and
+// the end need would otherwise sit in scalar registers, which run out in the loop.
+__device__ __forceinline__ PagedP again() {
+  uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(at));
+  return *(const PagedP*)(__attribute__((address_space(4))) const PagedP*)at;
+}
+
 // Keys of request b that are visible, [lo, n), and its first part's first key.
 struct Span {
   int lo, n, first;
@@ -105,40 +116,45 @@ __device__ __forceinline__ Span span_of(const PagedP& p, int b) {
   return s;
 }
 
-template <int FMT, int DT, int DP, bool PAD, int RT>
-__global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
-  constexpr bool CODES = FMT != SVDQ_KV_VALUES;
+// NW: waves of a block.
+template <int FMT, int DT, int DP, bool PAD, int RT, int NW>
+__global__ __launch_bounds__(64 * NW, RT == 2 && DP == 128 ? 1 : 2) void paged_kernel(PagedP p) {
+  constexpr bool CODES = FMT != SVDQ_KV_VALUES, INT8 = FMT == SVDQ_KV_INT8;
   constexpr bool FP16 = CODES || DT == SVDQ_FP16;
   constexpr int ES = CODES ? 1 : 2;
   constexpr int KPL = 16 / ES, TK = 4 * KPL;     // keys of a lane and of a tile
   constexpr int NT = TK / 16;                    // score tiles
   constexpr int NC = DP * ES / 64;               // 16-byte pieces of K a lane reads of a key
-  constexpr int NS = DP / 32;                    // MFMA steps of a score tile
+  constexpr int NS = DP / 32;                    // MFMA steps of a score tile (INT8: as many, 64 wide, of two parts of Q)
   constexpr int ND = DP / 16;                    // element tiles of O
   constexpr int NU = TK / 32;                    // MFMA steps of O
+  constexpr int STEP = NW * TK;                  // keys from a wave's tile to its next
   constexpr float LIFT = kLift<FMT, DT>;
-  __shared__ float jo[4][16 * RT][DP + 4];
-  __shared__ float jm[4][16 * RT][2];
+  __shared__ __attribute__((aligned(16))) float jo[NW][16 * RT][DP + 4];
+  __shared__ float jm[NW][16 * RT][2];
   const svdq_paged_attention_args& a = p.a;
   const svdq_kv_cache& c = p.c;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lc = lane & 15, lu = lane >> 4;
-  const int id = xcd_order(blockIdx.x, gridDim.x);
-  const int sp = id % p.part.splits, rest = id / p.part.splits;
-  const int rb = rest % p.rows, grp = rest / p.rows, h = grp % c.heads, b = grp / c.heads;
-  const Span sn = span_of(p, b);
-  const int begin = sn.first + sp * p.part.share, end = min(sn.n, begin + p.part.share);
-  if (sp > 0 && begin >= end) return;            // no such part
+  // Which part, rows and (request, K/V head).  Divisions of a few instructions: by what
+  // the host worked out, or none where the divisor is 1.
+  const uint32_t id = xcd_order(blockIdx.x, gridDim.x);
+  const uint32_t rest = p.part.splits == 1 ? id : __umulhi(id, p.by_splits);
+  const int sp = id - rest * p.part.splits;
+  const uint32_t grp = p.rows == 1 ? rest : rest / p.rows;
+  const int rb = rest - grp * p.rows;
+  const uint32_t entry = p.a.B == 1 ? 0 : p.by_heads ? __umulhi(grp, p.by_heads) : grp / c.heads;
+  const int b = entry, h = grp - entry * c.heads;
   const int D = PAD ? c.D : DP;
-
-  // ---- Q as the B operand
+  // ---- Q: asked for before all else
   b4i qf[RT][NS];
-  float rq[RT];                                  // power of two taken out of a row
+  float rq[RT], slope[RT];                       // a row's factor
   int qh[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     qh[r] = h * p.G + min(rb * 16 * RT + 16 * r + lc, p.G - 1);
+    slope[r] = a.slopes ? a.slopes[qh[r]] * 1.44269504f : 0.f;
     const uint16_t* qp = a.q + b * a.q_batch + qh[r] * a.q_head;
     // the elements that meet K's piece of the same step in this lane
 #pragma unroll
@@ -147,28 +163,141 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
       qf[r][s] = (b4i){0, 0, 0, 0};
       if (!PAD || d < D) qf[r][s] = *reinterpret_cast<const b4i*>(qp + d);
     }
+  }
+
+  // page of key j of the request: -1 if there is none
+  const int32_t* table = a.table + b * a.table_row;
+  auto page_of = [&](int j) __attribute__((always_inline)) -> int {
+    const int page = table[min(j >> p.shift, a.T - 1)];
+    return (unsigned)page < (unsigned)c.pages ? page : -1;
+  };
+  const int mask = c.page - 1;
+  const int kg = KPL * (lc >> 2), vg = KPL * lu;   // keys of a tile whose pages the lane needs: K's, V's and the scores'
+
+  // Without a window the block's first key does not depend on the length, and the
+  // first pages are looked up while that is on its way.
+  int first = 0;
+  if (a.window > 0) first = span_of(p, b).first;
+  const int begin = first + sp * p.part.share;
+  int j = begin + TK * wave;
+  int kpage = page_of(j + kg), vpage = page_of(j + vg);   // pages of this tile and of the next
+  int knext = page_of(j + STEP + kg), vnext = page_of(j + STEP + vg);
+  const Span sn = span_of(p, b);
+  const int end = min(sn.n, begin + p.part.share);
+  if (sp > 0 && begin >= end) {                  // no such part: no weights
+    for (int r = threadIdx.x; r < 16 * RT && rb * 16 * RT + r < p.G; r += 64 * NW)
+      *reinterpret_cast<float2*>(p.part.ml + 2 * ((size_t)sp * ((size_t)a.B * a.Hq) + (size_t)b * a.Hq + h * p.G + rb * 16 * RT + r)) =
+          make_float2(kLow, 0.f);
+    return;
+  }
+
+  float m[RT], l[RT], iv = 0x1p126f;             // iv: 1 / the power of two that V's scales stay under
+  b4f o[RT][ND], ow[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    ow[r] = (b4f){0.f, 0.f, 0.f, 0.f};
+    m[r] = kLow;
+    l[r] = 0.f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[r][d] = (b4f){0.f, 0.f, 0.f, 0.f};
+  }
+
+  // ---- loads of the tile at j
+  b4i kw[NT][NC], vw[ND];
+  b4f ks[NT], vs[NT];
+  auto load_k = [&](int j, int page) __attribute__((always_inline)) {
+    const uint8_t* kp = static_cast<const uint8_t*>(c.k) +
+                        ES * (max(page, 0) * c.k_page + (((int64_t)h << p.shift) + ((j + kg + (lc & 3)) & mask)) * D) + 16 * lu;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        if (PAD) kw[t][i] = (b4i){0, 0, 0, 0};
+        if (!PAD || 64 * i + 16 * lu < ES * D) kw[t][i] = *reinterpret_cast<const b4i*>(kp + 4 * t * ES * D + 64 * i);
+      }
+  };
+  auto load_scales = [&](int j, int page) __attribute__((always_inline)) {
+    if constexpr (CODES) {
+      const int64_t at = max(page, 0) * c.scale_page + ((int64_t)h << p.shift) + ((j + vg) & mask);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        ks[t] = *reinterpret_cast<const b4f*>(c.k_scale + at + 4 * t);
+        vs[t] = *reinterpret_cast<const b4f*>(c.v_scale + at + 4 * t);
+      }
+    }
+  };
+  auto load_v = [&](int j, int page) __attribute__((always_inline)) {
+    const uint8_t* vp = static_cast<const uint8_t*>(c.v) +
+                        ES * (max(page, 0) * c.v_page + (((int64_t)h * D + lc) << p.shift) + ((j + vg) & mask));
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      if (PAD) vw[d] = (b4i){0, 0, 0, 0};
+      if (!PAD || 16 * d < D) vw[d] = *reinterpret_cast<const b4i*>(vp + ((size_t)(16 * d * ES) << p.shift));
+    }
+  };
+
+  if (j < end) {
+    load_k(j, kpage);
+    load_scales(j, vpage);
+    load_v(j, vpage);
+  }
+
+  // ---- Q as the B operand, while the first tile is on its way
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
     rq[r] = 1.f;
     if constexpr (CODES) {
-      float top = 0.f;
+      // largest magnitude of the row, as bits: infinities and NaN are the largest
+      typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 most = (u16x2){0, 0};
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        float x[8];
-        widen8<DT>(qf[r][s], x);
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (fabsf(x[i]) < __builtin_inff()) top = fmaxf(top, fabsf(x[i]));
-      }
-      top = row_max(top);
-      const int e = max((int)(__float_as_uint(top) >> 23), 1) - 127;   // top < 2^(e + 1)
-      rq[r] = top > 0.f ? ldexpf(1.f, e) : 1.f;
-      const float by = (top > 0.f ? ldexpf(1.f, -e) : 1.f) * p.qmul;
+        for (int i = 0; i < 4; ++i)
+          most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, qf[r][s][i] & 0x7FFF7FFF));
+      int tb = max((int)most[0], (int)most[1]);
+      tb = max(tb, __shfl_xor(tb, 16));
+      tb = max(tb, __shfl_xor(tb, 32));
+      const float mag = widen2<DT>((uint32_t)tb)[0];
+      const bool odd = tb >= (DT == SVDQ_BF16 ? 0x7F80 : 0x7C00);
+      if constexpr (INT8) {
+        // x 32512 / top, rounded, as 256 times one 8-bit part and another: 0.5 in 32512 is
+        // off, a 250th of what K's own codes are off by; the sums of products are exact.
+        // Adding 1.5 2^23 + 128 rounds, and leaves the first part in byte 1 and the other,
+        // 128 more, in byte 0.
+        const float by = mag > 0.f ? fminf(32512.0f / mag, 0x1p126f) * p.qmul : 0.f;
+        rq[r] = odd ? __builtin_nanf("") : fmaxf(mag * (1.0f / 32512.0f), 0x1p-126f);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        float x[8];
-        widen8<DT>(qf[r][s], x);
+        for (int i = 0; i < NC; ++i) {
+          b4i parts[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = p.qmul != 0.f ? x[i] * by : 0.f;
-        qf[r][s] = narrow8<SVDQ_FP16>(x);
+          for (int w = 0; w < 4; ++w) {
+            const b4i& q4 = qf[r][2 * i + w / 2];
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[k] = __float_as_uint(fmaf(widen2<DT>((uint32_t)q4[2 * (w % 2) + k / 2])[k % 2], by, 0x1.8p23f + 128.0f));
+            const uint32_t x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100), y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100);
+            parts[0][w] = (int)__builtin_amdgcn_perm(y, x, 0x07050301);
+            parts[1][w] = (int)(__builtin_amdgcn_perm(y, x, 0x06040200) ^ 0x80808080u);
+          }
+          qf[r][2 * i] = parts[0];
+          qf[r][2 * i + 1] = parts[1];
+        }
+      } else {
+        // to [1, 2) by a power of two
+        const int e = max((int)(__float_as_uint(mag) >> 23), 1) - 127;
+        rq[r] = odd ? __builtin_nanf("") : __uint_as_float((uint32_t)(e + 127) << 23);
+        const float by = ldexpf(p.qmul, -e);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          float x[8];
+          widen8<DT>(qf[r][s], x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] *= by;
+          qf[r][s] = narrow8<SVDQ_FP16>(x);
+        }
       }
     } else if (!(p.qmul > 0.f)) {
 #pragma unroll
@@ -177,101 +306,74 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
         for (int i = 0; i < 4; ++i) qf[r][s][i] = p.flip ? qf[r][s][i] ^ (int)0x80008000 : 0;
     }
   }
-  float slope[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) slope[r] = a.slopes ? a.slopes[qh[r]] * 1.44269504f : 0.f;
 
-  float m[RT], l[RT], iv = 0x1p126f;             // iv: 1 / the power of two that V's scales stay under
-  b4f o[RT][ND];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    m[r] = kLow;
-    l[r] = 0.f;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) o[r][d] = (b4f){0.f, 0.f, 0.f, 0.f};
-  }
-
-  // page of key j of the request: -1 if there is none
-  const int32_t* table = a.table + b * a.table_row;
-  auto page_of = [&](int j) -> int {
-    const int page = table[min(j >> p.shift, a.T - 1)];
-    return (unsigned)page < (unsigned)c.pages ? page : -1;
-  };
-  const int mask = c.page - 1;
-  const int krow = KPL * (lc >> 2) + (lc & 3);   // key of the lane's row of score tile 0
-
-  for (int j0 = begin + TK * wave; j0 < end; j0 += 4 * TK) {
-    // ---- loads
-    const int kj = j0 + KPL * (lc >> 2), vj = j0 + KPL * lu;
-    const int kpage = page_of(kj), vpage = page_of(vj);
-    b4i kw[NT][NC], vw[ND];
-    b4f ks[NT], vs[NT];
-    {
-      const uint8_t* kp = static_cast<const uint8_t*>(c.k) +
-                          ES * (max(kpage, 0) * c.k_page + (((int64_t)h << p.shift) + ((j0 + krow) & mask)) * D) + 16 * lu;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          kw[t][i] = (b4i){0, 0, 0, 0};
-          if (!PAD || 64 * i + 16 * lu < ES * D) kw[t][i] = *reinterpret_cast<const b4i*>(kp + 4 * t * ES * D + 64 * i);
-        }
-      const uint8_t* vp = static_cast<const uint8_t*>(c.v) +
-                          ES * (max(vpage, 0) * c.v_page + (((int64_t)h * D + lc) << p.shift) + (vj & mask));
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        vw[d] = (b4i){0, 0, 0, 0};
-        if (!PAD || 16 * d < D) vw[d] = *reinterpret_cast<const b4i*>(vp + ((size_t)(16 * d * ES) << p.shift));
-      }
-      if constexpr (CODES) {
-        const int64_t at = max(vpage, 0) * c.scale_page + ((int64_t)h << p.shift) + (vj & mask);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          ks[t] = *reinterpret_cast<const b4f*>(c.k_scale + at + 4 * t);
-          vs[t] = *reinterpret_cast<const b4f*>(c.v_scale + at + 4 * t);
-        }
-      }
-    }
+  // The tile at j, whose loads are under way.  MORE: another follows, and each of its
+  // operands is asked for as soon as this tile's has been used, into the same registers.
+  auto tile = [&](int j, auto more) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(more)::value;
+    
+    const int vj = j + vg;
     // keys [lo, hi) of the lane's are visible
     const int lo = vpage >= 0 ? sn.lo - vj : KPL, hi = vpage >= 0 ? end - vj : 0;
     const bool cut = __any(lo > 0 || hi < KPL);
-    if (cut) {
-      // what is hidden takes no part, whatever is there
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t keep = 0;
-#pragma unroll
-        for (int k = 0; k < 4 / ES; ++k) {
-          const int x = 4 / ES * i + k;
-          if (x >= lo && x < hi) keep |= (ES == 1 ? 0xFFu : 0xFFFFu) << (8 * ES * k);
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d) vw[d][i] &= (int)keep;
-      }
-      if constexpr (CODES) {
-#pragma unroll
-        for (int x = 0; x < KPL; ++x)
-          if (x < lo || x >= hi) vs[x / 4][x % 4] = 0.f;
-      }
+    int kafter = -1, vafter = -1;
+    if constexpr (MORE) {
+      kafter = page_of(j + 2 * STEP + kg);
+      vafter = page_of(j + 2 * STEP + vg);
     }
 
     // ---- scores
     b4f s[RT][NT];
+    if constexpr (INT8) {
+      b4i x[RT][NT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+      for (int part = 0; part < 2; ++part) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) s[r][t] = (b4f){0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < NC; ++i)
 #pragma unroll
-    for (int st = 0; st < NS; ++st)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        b4i kf;
-        if constexpr (CODES) kf = widen_codes<FMT>(kw[t][st / 2][2 * (st % 2)], kw[t][st / 2][2 * (st % 2) + 1]);
-        else kf = kw[t][st];
+            for (int r = 0; r < RT; ++r) {
+              if (part == 0 && i == 0) x[r][t] = (b4i){0, 0, 0, 0};
+              x[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kw[t][i], qf[r][2 * i + part], x[r][t], 0, 0, 0);
+            }
+        if (part == 0)
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r][t] = mma16<FP16>(kf, qf[r][st], s[r][t]);
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[r][t] <<= 8;   // at most 128 x 127 x 128 x 256 < 2^30
       }
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[r][t][i] = (float)x[r][t][i];
+    } else {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) s[r][t] = (b4f){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < NS; ++st)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          b4i kf;
+          if constexpr (CODES) kf = widen_codes<FMT>(kw[t][st / 2][2 * (st % 2)], kw[t][st / 2][2 * (st % 2) + 1]);
+          else kf = kw[t][st];
+#pragma unroll
+          for (int r = 0; r < RT; ++r) s[r][t] = mma16<FP16>(kf, qf[r][st], s[r][t]);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MORE) load_k(j + STEP, knext);
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (CODES) {
+      if (cut) {
+#pragma unroll
+        for (int x = 0; x < KPL; ++x)
+          if (x < lo || x >= hi) vs[x / 4][x % 4] = 0.f;
+      }
       // room for V's scales
       float big = 0.f;
 #pragma unroll
@@ -281,11 +383,14 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
       if (__any(big * iv > 1.0f)) {
         big = row_max(big);
         const int e = min(max((int)(__float_as_uint(big) >> 23) - 126, -126), 126);   // big < 2^e
-        const float next = ldexpf(1.f, -e), f = next / iv;
+        const float next = __uint_as_float((uint32_t)(127 - e) << 23);
+        const float f = next * (1.0f / iv);   // (iv is a power of two: exact, or 0)
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RT; ++r) {
+          ow[r] *= f;
 #pragma unroll
           for (int d = 0; d < ND; ++d) o[r][d] *= f;
+        }
         iv = next;
       }
     }
@@ -300,19 +405,32 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[r][t][i] = s[r][t][i] * ks[t][i] * rq[r];
         }
-      if (!(a.softcap > 0.f || a.slopes)) {
+      if (a.softcap > 0.f) {
+        const PagedP p = again();
+        if (p.a.softcap <= kSmallCap) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[r][t][i] = by_exp(p, s[r][t][i]);
+        } else {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = s[r][t][i], near = by_series(p, x), far = by_exp(p, x);
+              s[r][t][i] = fabsf(x * p.c4) <= 1.0f ? near : far;
+            }
+        }
+      } else {
 #pragma unroll
         for (int t = 0; t < NT; ++t) s[r][t] *= p.c1;
-      } else {
+      }
+      if (a.slopes) {
+        const float from = (float)(sn.n - 1 - vj);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float x = s[r][t][i];
-            x = a.softcap > 0.f ? capped(p, x) : x * p.c1;
-            if (a.slopes) x = fmaf(-slope[r], (float)(sn.n - 1 - vj - 4 * t - i), x);
-            s[r][t][i] = x;
-          }
+          for (int i = 0; i < 4; ++i) s[r][t][i] = fmaf(-slope[r], from - (float)(4 * t + i), s[r][t][i]);
       }
       if (cut) {
 #pragma unroll
@@ -331,6 +449,7 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
         const float f = exp2_(m[r] - up);
         m[r] = up;
         l[r] *= f;
+        ow[r] *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[r][d] *= f;
       }
@@ -344,11 +463,30 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
           if constexpr (CODES) w[i] *= vs[t][i] * iv;
         }
         // To the product with V the weights go in 16 bits, as the matrix unit takes them
-        pf[r][t / 2][2 * (t % 2)] = (int)narrow2<FP16 ? SVDQ_FP16 : SVDQ_BF16>(w[0], w[1]);
-        pf[r][t / 2][2 * (t % 2) + 1] = (int)narrow2<FP16 ? SVDQ_FP16 : SVDQ_BF16>(w[2], w[3]);
+        constexpr int T16 = FP16 ? SVDQ_FP16 : SVDQ_BF16, I1 = INT8 ? 2 : 1, I2 = INT8 ? 1 : 2;   // in V's order
+        pf[r][t / 2][2 * (t % 2)] = (int)narrow2<T16>(w[0], w[I1]);
+        pf[r][t / 2][2 * (t % 2) + 1] = (int)narrow2<T16>(w[I2], w[3]);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MORE) load_scales(j + STEP, vnext);
+    __builtin_amdgcn_sched_barrier(0);
+
     // ---- values
+    if (cut && !INT8) {                            // (codes of INT8 are all finite)
+      // what is hidden takes no part, whatever is there
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t keep = 0;
+#pragma unroll
+        for (int k = 0; k < 4 / ES; ++k) {
+          const int x = 4 / ES * i + k;
+          if (x >= lo && x < hi) keep |= (ES == 1 ? 0xFFu : 0xFFFFu) << (8 * ES * k);
+        }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) vw[d][i] &= (int)keep;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < NU; ++u)
 #pragma unroll
@@ -359,6 +497,27 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
 #pragma unroll
         for (int r = 0; r < RT; ++r) o[r][d] = mma16<FP16>(vf, pf[r][u], o[r][d]);
       }
+    if constexpr (INT8) {
+      // -128 2^-24 times the sum of the weights as rounded
+      const int less = (int)0x80808080;
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) ow[r] = mma16<true>((b4i){less, less, less, less}, pf[r][u], ow[r]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MORE) {
+      load_v(j + STEP, vnext);
+      __builtin_amdgcn_sched_barrier(0);
+      kpage = knext;
+      vpage = vnext;
+      knext = kafter;
+      vnext = vafter;
+    }
+  };
+  if (j < end) {
+    for (; j + STEP < end; j += STEP) tile(j, std::true_type{});
+    tile(j, std::false_type{});
   }
 
   // ---- join the waves: means and (maximum, sum) through LDS
@@ -366,40 +525,41 @@ __global__ __launch_bounds__(256, 2) void paged_kernel(PagedP p) {
   for (int r = 0; r < RT; ++r) {
     const float sum = row_sum(l[r]);
     // a mean of codes is at most 448, so the scale comes back after the division
-    const float by = sum != 0.f ? 1.0f / sum : 0.f, back = CODES ? 1.0f / iv : 1.f;
+    const float by = sum != 0.f ? 1.0f / sum : 0.f, back = CODES ? (INT8 ? 0x1p24f : 1.0f) / iv : 1.f;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
       *reinterpret_cast<b4f*>(&jo[wave][16 * r + lc][16 * d + 4 * lu]) =
-          (b4f){o[r][d][0] * by * back, o[r][d][1] * by * back, o[r][d][2] * by * back, o[r][d][3] * by * back};
+          (INT8 ? o[r][d] + ow[r] : o[r][d]) * by * back;
     if (lu == 0) {
       jm[wave][16 * r + lc][0] = m[r];
       jm[wave][16 * r + lc][1] = sum;
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * RT * (DP / 4); i += 256) {
+  const PagedP e = again();
+  for (int i = threadIdx.x; i < 16 * RT * (DP / 4); i += 64 * NW) {
     const int r = i / (DP / 4), d = 4 * (i % (DP / 4)), row = rb * 16 * RT + r;
-    if (row >= p.G || d >= D) continue;
+    if (row >= e.G || d >= D) continue;
     float up = jm[0][r][0], sum = 0.f;
 #pragma unroll
-    for (int w = 1; w < 4; ++w) up = fmaxf(up, jm[w][r][0]);
+    for (int w = 1; w < NW; ++w) up = fmaxf(up, jm[w][r][0]);
     b4f x = (b4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < NW; ++w) {
       const float f = jm[w][r][1] * exp2_(jm[w][r][0] - up);
       sum += f;
       x += *reinterpret_cast<const b4f*>(&jo[w][r][d]) * f;
     }
     x *= sum != 0.f ? 1.0f / sum : 0.f;
-    const size_t at = (size_t)b * a.Hq + h * p.G + row;
-    if (p.part.splits > 1) {
-      const size_t pt = (size_t)sp * ((size_t)a.B * a.Hq) + at;
-      *reinterpret_cast<b4f*>(p.part.o + pt * DP + d) = x;
-      if (d == 0) *reinterpret_cast<float2*>(p.part.ml + 2 * pt) = make_float2(up, sum);
+    const size_t at = (size_t)b * e.a.Hq + h * e.G + row;
+    if (e.part.splits > 1) {
+      const size_t pt = (size_t)sp * ((size_t)a.B * e.a.Hq) + at;
+      *reinterpret_cast<b4f*>(e.part.o + pt * DP + d) = x;
+      if (d == 0) *reinterpret_cast<float2*>(e.part.ml + 2 * pt) = make_float2(up, sum);
     } else {
-      *reinterpret_cast<uint2*>(a.o + b * a.o_batch + (h * p.G + row) * a.o_head + d) =
+      *reinterpret_cast<uint2*>(e.a.o + b * e.a.o_batch + (h * e.G + row) * e.a.o_head + d) =
           make_uint2(narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3]));
-      if (d == 0 && a.lse) a.lse[at] = sum != 0.f ? (up + __log2f(sum)) * 0.693147181f : -__builtin_inff();
+      if (d == 0 && e.a.lse) e.a.lse[at] = sum != 0.f ? (up + __log2f(sum)) * 0.693147181f : -__builtin_inff();
     }
   }
 }
@@ -419,16 +579,11 @@ __global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
   if (live) {
-    const Span sn = span_of(p, (int)(at / a.Hq));
-    const int parts = min(p.part.splits, max(1, (sn.n - sn.first + p.part.share - 1) / p.part.share));
-    for (int s = g; s < parts; s += across) {
+    for (int s = g; s < p.part.splits; s += across) {
       const float2 ml = *reinterpret_cast<const float2*>(p.part.ml + 2 * (s * rows + at));
       const float* op = p.part.o + (s * rows + at) * DP + d;
-      b4f x = (b4f){0.f, 0.f, 0.f, 0.f}, y = x;
-      if (d < p.c.D) {
-        x = *reinterpret_cast<const b4f*>(op);
-        y = *reinterpret_cast<const b4f*>(op + 4);
-      }
+      const b4f x = *reinterpret_cast<const b4f*>(op), y = *reinterpret_cast<const b4f*>(op + 4);
+      if (ml.y == 0.f) continue;                 // no keys, and nothing stored; or no weights
       const float up = fmaxf(top, ml.x), f0 = exp2_(top - up), f = ml.y * exp2_(ml.x - up);
       sum = fmaf(sum, f0, f);
 #pragma unroll
@@ -470,18 +625,46 @@ int padded_dim(int32_t D) { return D <= 64 ? 64 : 128; }
 // The arrangement of a call.  keys: at most so many of a request are visible.
 struct PagedPlan {
   int G, rows, share, splits;
+  bool wide;                // eight waves a block instead of four
 };
+// Waves of a block and parts of a row of keys by the least time, in ns: rounds of as
+// many blocks as the chip holds, each with about 3000 of start and end; a wave's tiles
+// at 2800 each by itself, or at the rate at which all waves' tiles come from memory;
+// the join.  (Measured, us, four waves -> eight: 131072 keys x 8 heads of 128 in 64 and
+// 32 parts 57.1 -> 55.5; 16 requests of up to 16384 in 4 and 2 parts 73.6 -> 71.1; 64 of
+// 1024 in one 19.8 -> 23.7.  One request of 1024 keys in 4 parts of four waves 9.2, in
+// one of eight 10.4.)
 PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   PagedPlan p;
   p.G = Hq / c.heads;
   p.rows = p.G <= 16 ? 1 : (p.G + 31) / 32;
   const int64_t blocks = (int64_t)B * c.heads * p.rows;
-  // Blocks that the chip holds twice over, as lengths differ, and at least 1024 keys
-  // each: shorter parts cost more in their start and end, and in the join.
-  const int64_t want = (4 * kCus + blocks - 1) / blocks;
-  int64_t share = ((keys + want - 1) / want + 255) / 256 * 256;
-  if (share < 1024) share = 1024;
-  p.share = (int)share;
+  const int64_t tile_keys = c.format == SVDQ_KV_VALUES ? 32 : 64, tile_bytes = 128 * padded_dim(c.D) + 512;
+  const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
+  int64_t least = 0;
+  p.splits = 1;
+  p.wide = false;
+  for (int wide = 0; wide < (p.rows == 1 && p.G <= 16 ? 2 : 1); ++wide) {
+    const int64_t waves = wide ? 8 : 4, slots = (p.G > 16 || wide ? 1 : 2) * kCus;
+    int64_t most = (tiles + waves - 1) / waves;
+    if (most > 64) most = 64;
+    if (most > 2 * kCus / blocks) most = 2 * kCus / blocks;
+    for (int64_t k = 1; k == 1 || k <= most; ++k) {
+      const int64_t n = blocks * k, steps = ((tiles + k - 1) / k + waves - 1) / waves;
+      auto round = [&](int64_t at_once) {
+        const int64_t bytes = at_once * waves * tile_bytes / 5400;   // ns a tile at 5.4 TB/s
+        return 3000 + steps * (bytes > 2800 ? bytes : 2800);
+      };
+      const int64_t cost = n / slots * round(slots) + (n % slots ? round(n % slots) : 0) + (k > 1 ? 2000 + 30 * k : 0);
+      if (least == 0 || cost < least) {
+        least = cost;
+        p.splits = (int)k;
+        p.wide = wide;
+      }
+    }
+  }
+  const int64_t share = ((keys + p.splits - 1) / p.splits + 255) / 256 * 256;
+  p.share = (int)(share > 0 ? share : 256);
   p.splits = (int)((keys + share - 1) / share);
   if (p.splits < 1) p.splits = 1;
   return p;
@@ -495,8 +678,9 @@ size_t plan_bytes(const PagedPlan& p, int32_t B, int32_t Hq, int32_t D) {
 template <int FMT, int DT, int DP, bool PAD>
 svdq_status launch_rows(const PagedP& p, const PagedPlan& pl, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.a.B * p.c.heads * pl.rows * pl.splits));
-  if (pl.G <= 16) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1>), grid, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 2>), grid, dim3(256), 0, st, p);
+  if (pl.G > 16) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 2, 4>), grid, dim3(256), 0, st, p);
+  else if (pl.wide) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1, 8>), grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1, 4>), grid, dim3(256), 0, st, p);
   svdq_status s = launched();
   if (s == SVDQ_OK && pl.splits > 1) {
     int across = 1;
@@ -567,6 +751,13 @@ extern "C" svdq_status svdq_paged_attention(const svdq_kv_cache* cache, const sv
   p.G = pl.G;
   p.rows = pl.rows;
   p.shift = __builtin_ctz(cache->page);
+  // x / d is the upper half of x ceil(2^32 / d) as long as x d < 2^32; x < 2^24
+  auto over = [](uint32_t d, uint64_t most) -> uint32_t {
+    return d > 1 && most * d < (1ull << 32) ? (uint32_t)(((1ull << 32) + d - 1) / d) : 0;
+  };
+  const uint64_t groups = (uint64_t)a->B * cache->heads;
+  p.by_splits = over(pl.splits, groups * pl.rows * pl.splits);
+  p.by_heads = over(cache->heads, groups);
   set_score(&p, a->scale, a->softcap);
   p.part.share = pl.share;
   p.part.splits = pl.splits;

@@ -2,13 +2,15 @@
 
 Bound.  With u = 2^-24: a score is off by (2 D + 16) u times its magnitudes
 (products summed in the matrix unit, the scales' products, the cap, the bias), and for
-codes by what a query element below fp16's range loses, 2^-25 of the row's largest
-times sum |k|; a weight by e^2d - 1 < 3 d relative with d that error plus 2^-21 for the
-exponential.  Rounding the weights adds 2^-11 (fp16: codes and fp16 values) or 2^-8
-(bf16 values); adding n weighted values in fp32 2 n u at most, the means of waves and
-parts 16 u.  All of these are relative to mean |v| + |o|.  The largest weight is at
-least 2^6 in fp16, and weights below fp16's range lose 2^-25 each, next to a value of at
-most 4 max |v| in the units of the product: n 2^-29 max |v|.  The store adds half an ulp.
+codes by what the query loses: E4M3 2^-25 of the row's largest element times sum |k|
+(fp16's smallest step at [1, 2)), INT8 2^-16 of it (half a step of 1 / 32512); a weight by
+e^2d - 1 < 3 d relative with d that error plus 2^-21 for the exponential.  Rounding the
+weights adds 2^-11 (fp16: codes and fp16 values) or 2^-8 (bf16 values); adding n weighted
+values in fp32 2 n u at most, the means of waves and parts 16 u.  All of these are relative to
+mean |v| + |o|.  INT8 values are added as code + 128 <= 255 and 128 times the weights is
+taken out: 2 n u of 2 max |v| each.  The largest weight is at least 2^6 in fp16, and weights
+below fp16's range lose 2^-25 each, next to a value of at most 4 max |v| in the units of
+the product: n 2^-29 max |v|.  The store adds half an ulp.
 The logarithm of the sum is off by d + 2 n u, by 2^-17 for the logarithm of a sum up to 2^38
 and by 2^-22 of itself."""
 import numpy as np
@@ -46,10 +48,10 @@ def _check(o, lse, qv, nc, table, kv_len, fmt, kind, what, **kw):
     fine = lambda a: np.abs(a[np.isfinite(a)]).max(initial=0.0)
     d = (2 * D + 16) * U * weight + 2.0**-21
     if fmt != "values":
-        d = d + 2.0**-25 * np.abs(qv).max(-1) * abs(kw["scale"]) * fine(np.abs(k).sum(-1))
+        d = d + (2.0**-16 if fmt == "int8" else 2.0**-25) * np.abs(qv).max(-1) * abs(kw["scale"]) * fine(np.abs(k).sum(-1))
     n = seen[..., None]
     rel = 3 * d[..., None] + (2.0**-8 if fmt == "values" and kind == "bf16" else 2.0**-11) + (2 * n + 16) * U
-    e = rel * (mean + np.abs(want))
+    e = rel * (mean + np.abs(want)) + (4 * n * U * fine(v) if fmt == "int8" else 0.0)
     if fmt != "values" or kind == "fp16":
         e = e + n * 2.0**-29 * fine(v)
     assert_within(values(o), want, np.where(n > 0, e + half_ulp(np.abs(want) + e, kind), 0.0), what)
