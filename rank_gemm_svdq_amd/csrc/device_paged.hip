@@ -116,9 +116,8 @@ __device__ __forceinline__ Span span_of(const PagedP& p, int b) {
   return s;
 }
 
-// NW: waves of a block.
-template <int FMT, int DT, int DP, bool PAD, int RT, int NW>
-__global__ __launch_bounds__(64 * NW, RT == 2 && DP == 128 ? 1 : 2) void paged_kernel(PagedP p) {
+template <int FMT, int DT, int DP, bool PAD, int RT>
+__global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kernel(PagedP p) {
   constexpr bool CODES = FMT != SVDQ_KV_VALUES, INT8 = FMT == SVDQ_KV_INT8;
   constexpr bool FP16 = CODES || DT == SVDQ_FP16;
   constexpr int ES = CODES ? 1 : 2;
@@ -128,7 +127,7 @@ __global__ __launch_bounds__(64 * NW, RT == 2 && DP == 128 ? 1 : 2) void paged_k
   constexpr int NS = DP / 32;                    // MFMA steps of a score tile (INT8: as many, 64 wide, of two parts of Q)
   constexpr int ND = DP / 16;                    // element tiles of O
   constexpr int NU = TK / 32;                    // MFMA steps of O
-  constexpr int STEP = NW * TK;                  // keys from a wave's tile to its next
+  constexpr int NW = 4, STEP = NW * TK;          // waves, and keys from a wave's tile to its next
   constexpr float LIFT = kLift<FMT, DT>;
   __shared__ __attribute__((aligned(16))) float jo[NW][16 * RT][DP + 4];
   __shared__ float jm[NW][16 * RT][2];
@@ -625,15 +624,17 @@ int padded_dim(int32_t D) { return D <= 64 ? 64 : 128; }
 // The arrangement of a call.  keys: at most so many of a request are visible.
 struct PagedPlan {
   int G, rows, share, splits;
-  bool wide;                // eight waves a block instead of four
 };
-// Waves of a block and parts of a row of keys by the least time, in ns: rounds of as
-// many blocks as the chip holds, each with about 3000 of start and end; a wave's tiles
-// at 2800 each by itself, or at the rate at which all waves' tiles come from memory;
-// the join.  (Measured, us, four waves -> eight: 131072 keys x 8 heads of 128 in 64 and
-// 32 parts 57.1 -> 55.5; 16 requests of up to 16384 in 4 and 2 parts 73.6 -> 71.1; 64 of
-// 1024 in one 19.8 -> 23.7.  One request of 1024 keys in 4 parts of four waves 9.2, in
-// one of eight 10.4.)
+// Parts of a row of keys by the least time, in ns.  A compute unit brings in what the four
+// tiles of a block's step need in 1600 (heads of 128; what it can have under way at a
+// time bounds it, and a second block beside the first does not help), or all of them at the rate of
+// the memory, of which a batch's lengths leave about 0.7 in use; so blocks are as many to
+// a compute unit as the fullest has.  Start and end are 4500, 700 more for each block
+// after the first, and the join 2500 and 100 a part.
+// (us for 1, 2, 4, 8 .. parts: 4096 keys x 8 heads 28.5, 19.1, 13.1, 11.3, 10.3;
+// 131072 x 8 in 16, 32, 48, 64 parts 82.7, 55.8, 66.2, 57.2; 16 requests of up to 16384 in
+// 1, 2, 3, 4: 111, 79, 95, 80; 64 of 1024 20.4, 26.0, 33.4; 40 of 4096 64.9, 60.1, 58.6, 62.5.
+// Eight waves a block took the same time at as many blocks.)
 PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   PagedPlan p;
   p.G = Hq / c.heads;
@@ -641,32 +642,20 @@ PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   const int64_t blocks = (int64_t)B * c.heads * p.rows;
   const int64_t tile_keys = c.format == SVDQ_KV_VALUES ? 32 : 64, tile_bytes = 128 * padded_dim(c.D) + 512;
   const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
-  int64_t least = 0;
-  p.splits = 1;
-  p.wide = false;
-  for (int wide = 0; wide < (p.rows == 1 && p.G <= 16 ? 2 : 1); ++wide) {
-    const int64_t waves = wide ? 8 : 4, slots = (p.G > 16 || wide ? 1 : 2) * kCus;
-    int64_t most = (tiles + waves - 1) / waves;
-    if (most > 64) most = 64;
-    if (most > 2 * kCus / blocks) most = 2 * kCus / blocks;
-    for (int64_t k = 1; k == 1 || k <= most; ++k) {
-      const int64_t n = blocks * k, steps = ((tiles + k - 1) / k + waves - 1) / waves;
-      auto round = [&](int64_t at_once) {
-        const int64_t bytes = at_once * waves * tile_bytes / 5400;   // ns a tile at 5.4 TB/s
-        return 3000 + steps * (bytes > 2800 ? bytes : 2800);
-      };
-      const int64_t cost = n / slots * round(slots) + (n % slots ? round(n % slots) : 0) + (k > 1 ? 2000 + 30 * k : 0);
-      if (least == 0 || cost < least) {
-        least = cost;
-        p.splits = (int)k;
-        p.wide = wide;
-      }
+  const int64_t alone = 200 + tile_bytes * 83 / 1000, full = 4 * kCus * tile_bytes * (B > 1 ? 7 : 10) / 54000;
+  int64_t least = 0, best = 1;
+  for (int64_t k = 1; k <= 128 && (k == 1 || (4 * k < tiles + 4 && blocks * (k - 1) < 4 * kCus)); ++k) {
+    const int64_t n = blocks * k, each = (n + kCus - 1) / kCus, steps = ((tiles + k - 1) / k + 3) / 4;
+    const int64_t step = n >= kCus ? full : full * n / kCus;
+    const int64_t cost = each * (steps * (step > alone ? step : alone) + 700) + 3800 + (k > 1 ? 2500 + 100 * (k < 16 ? k : 16) + 8 * k : 0);
+    if (k == 1 || cost < least) {
+      least = cost;
+      best = k;
     }
   }
-  const int64_t share = ((keys + p.splits - 1) / p.splits + 255) / 256 * 256;
-  p.share = (int)(share > 0 ? share : 256);
+  const int64_t share = ((keys + best - 1) / best + 255) / 256 * 256;
+  p.share = (int)share;
   p.splits = (int)((keys + share - 1) / share);
-  if (p.splits < 1) p.splits = 1;
   return p;
 }
 size_t plan_bytes(const PagedPlan& p, int32_t B, int32_t Hq, int32_t D) {
@@ -678,9 +667,8 @@ size_t plan_bytes(const PagedPlan& p, int32_t B, int32_t Hq, int32_t D) {
 template <int FMT, int DT, int DP, bool PAD>
 svdq_status launch_rows(const PagedP& p, const PagedPlan& pl, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)p.a.B * p.c.heads * pl.rows * pl.splits));
-  if (pl.G > 16) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 2, 4>), grid, dim3(256), 0, st, p);
-  else if (pl.wide) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1, 8>), grid, dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1, 4>), grid, dim3(256), 0, st, p);
+  if (pl.G <= 16) hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 1>), grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((paged_kernel<FMT, DT, DP, PAD, 2>), grid, dim3(256), 0, st, p);
   svdq_status s = launched();
   if (s == SVDQ_OK && pl.splits > 1) {
     int across = 1;

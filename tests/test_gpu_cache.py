@@ -35,7 +35,10 @@ def _tokens(M, heads, D, kind, seed, strided=True):
 WRITES = [  # tokens, requests, heads, D, page, pages of a request
     (1, 1, 1, 16, 16, 1), (3, 3, 2, 128, 64, 2), (16, 16, 8, 128, 64, 3), (17, 2, 1, 64, 16, 4), (61, 1, 3, 80, 32, 4),
     (64, 1, 2, 128, 64, 2), (65, 4, 5, 96, 128, 1), (200, 3, 4, 112, 16, 9), (333, 2, 2, 48, 256, 2), (700, 1, 30, 64, 64, 13),
-    (1100, 5, 24, 128, 64, 6)]
+    (1100, 5, 24, 128, 64, 6),
+    # enough tokens and heads for the kernel that turns values through LDS: odd sizes and scattered places too
+    (130, 2, 48, 80, 32, 4), (200, 7, 40, 112, 16, 9), (301, 3, 32, 64, 16, 9), (65, 1, 64, 128, 64, 3), (640, 4, 13, 96, 128, 2),
+    (129, 9, 43, 48, 256, 1)]
 
 
 @pytest.mark.parametrize("shape", WRITES)
@@ -63,24 +66,46 @@ def test_write_against_oracle(shape, fmt, kind):
 
 @pytest.mark.parametrize("first", range(0, 9))
 @pytest.mark.parametrize("fmt", ["int8", "values"])
-def test_runs_that_start_inside_a_group_of_places(first, fmt):
+@pytest.mark.parametrize("heads", [2, 64])
+def test_runs_that_start_inside_a_group_of_places(first, fmt, heads):
     """Prompts from any place on, over the ends of pages."""
-    cache = random_cache(6, 2, 32, 64, fmt, "bf16", 4)
+    cache = random_cache(6, heads, 32, 64, fmt, "bf16", 4)
     table = random_table(1, 6, 6, 5)
-    k, v = _tokens(150, 2, 64, "bf16", 6)
+    k, v = _tokens(150, heads, 64, "bf16", 6)
     pos, entry = np.arange(150) + first, np.zeros(150)
     want = S.write(numpy_of(cache), table, entry, pos, values(k), values(v), fmt)
     B.cache_write(cache, ints(table), ints(pos), k, v, entry=ints(entry))
     _same(cache, want, f"first {first}")
 
 
+def test_several_requests_with_runs_of_their_own_phase():
+    """Ragged prompts one after the other, padded rows between and behind them."""
+    cache = random_cache(40, 48, 16, 64, "int8", "bf16", 4)
+    table = random_table(5, 8, 40, 5)
+    entry, pos = [], []
+    for e, (start, n) in enumerate(((3, 50), (0, 41), (14, 77), (5, 1), (9, 100))):
+        entry += [e] * n + [0] * 5
+        pos += list(range(start, start + n)) + [-1] * 5
+    k, v = _tokens(len(pos), 48, 64, "bf16", 6)
+    want = S.write(numpy_of(cache), table, np.array(entry), np.array(pos), values(k), values(v), "int8")
+    B.cache_write(cache, ints(table), ints(pos), k, v, entry=ints(entry))
+    _same(cache, want, "ragged")
+    # the same tokens in an order without runs
+    o = np.random.default_rng(7).permutation(len(pos))
+    other = random_cache(40, 48, 16, 64, "int8", "bf16", 4)
+    B.cache_write(other, ints(table), ints(np.array(pos)[o]), k[torch.from_numpy(o).cuda()], v[torch.from_numpy(o).cuda()],
+                  entry=ints(np.array(entry)[o]))
+    _same(other, want, "shuffled")
+
+
 @pytest.mark.parametrize("fmt", ["int8", "fp8", "values"])
-def test_places_that_do_not_exist_are_passed_over(fmt):
-    cache = random_cache(5, 2, 16, 32, fmt, "fp16", 7)
+@pytest.mark.parametrize("heads", [2, 130])
+def test_places_that_do_not_exist_are_passed_over(fmt, heads):
+    cache = random_cache(5, heads, 16, 32, fmt, "fp16", 7)
     table = np.array([[0, -1, 7], [2, 5, 4], [3, 2**31 - 1, -2**31]], np.int32)
     pos = np.array([0, 16, 33, 47, 48, 2**31 - 1, -1, -2**31, 3, 17, 40, 15, 31, 32, 0, 0])
     entry = np.array([0, 0, 0, 0, 0, 0, 0, 0, 1, 1, 1, 2, 2, 2, 3, -1])
-    k, v = _tokens(16, 2, 32, "fp16", 8)
+    k, v = _tokens(16, heads, 32, "fp16", 8)
     before = numpy_of(cache)
     want = S.write(before, table, entry, pos, values(k), values(v), fmt)
     assert len(S.places(table, entry, pos, 5, 16)) == 4
@@ -93,7 +118,8 @@ def test_places_that_do_not_exist_are_passed_over(fmt):
 
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
-def test_vectors_of_any_magnitude(fmt, kind):
+@pytest.mark.parametrize("heads", [1, 130])
+def test_vectors_of_any_magnitude(fmt, kind, heads):
     """Zeros, subnormals, the largest values, halfway quotients, infinities and NaN."""
     D, big = 64, torch.finfo(DTYPES[kind]).max
     rng = np.random.default_rng(9)
@@ -104,10 +130,10 @@ def test_vectors_of_any_magnitude(fmt, kind):
             np.r_[2.0**-24, np.zeros(D - 1)], np.r_[254.0, np.arange(D - 1) * 2 + 1]]
     if kind == "bf16":
         rows += [rng.standard_normal(D) * 2.0**e for e in (-133, -128, -126, -122, -119, -118, -117, 100, 120)]
-    x = np.stack(rows)[:, None]
+    x = np.repeat(np.stack(rows)[:, None], heads, axis=1)
     t, xv = device(x, kind)
     M = len(rows)
-    cache = random_cache(2, 1, 32, D, fmt, kind, 10)
+    cache = random_cache(2, heads, 32, D, fmt, kind, 10)
     table, pos, entry = np.array([[1]]), np.arange(M), np.zeros(M)
     want = S.write(numpy_of(cache), table, entry, pos, xv, xv[::-1], fmt)
     B.cache_write(cache, ints(table), ints(pos), t, t.flip(0).contiguous(), entry=ints(entry))
