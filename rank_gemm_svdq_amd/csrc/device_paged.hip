@@ -626,11 +626,12 @@ struct PagedPlan {
   int G, rows, share, splits;
 };
 // Parts of a row of keys by the least time, in ns.  A compute unit brings in what the four
-// tiles of a block's step need in 1600 (heads of 128; what it can have under way at a
-// time bounds it, and a second block beside the first does not help), or all of them at the rate of
-// the memory, of which a batch's lengths leave about 0.7 in use; so blocks are as many to
-// a compute unit as the fullest has.  Start and end are 4500, 700 more for each block
-// after the first, and the join 2500 and 100 a part.
+// tiles of a block's step need in 2000 (heads of 128; 1600 from the last-level cache, 2400
+// from memory; what it can have under way at a time bounds it, and a second block
+// beside the first does not help), or all of them at the rate of the memory, of which a
+// batch's lengths leave about 0.7 in use; so blocks are as many to a compute unit as the
+// fullest has.  Start and end are 4500, 700 more for each block after the first, and the
+// join 2500, 100 a part up to 16 and 8 a part.
 // (us for 1, 2, 4, 8 .. parts: 4096 keys x 8 heads 28.5, 19.1, 13.1, 11.3, 10.3;
 // 131072 x 8 in 16, 32, 48, 64 parts 82.7, 55.8, 66.2, 57.2; 16 requests of up to 16384 in
 // 1, 2, 3, 4: 111, 79, 95, 80; 64 of 1024 20.4, 26.0, 33.4; 40 of 4096 64.9, 60.1, 58.6, 62.5.
@@ -642,7 +643,7 @@ PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   const int64_t blocks = (int64_t)B * c.heads * p.rows;
   const int64_t tile_keys = c.format == SVDQ_KV_VALUES ? 32 : 64, tile_bytes = 128 * padded_dim(c.D) + 512;
   const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
-  const int64_t alone = 200 + tile_bytes * 83 / 1000, full = 4 * kCus * tile_bytes * (B > 1 ? 7 : 10) / 54000;
+  const int64_t alone = 250 + tile_bytes * 104 / 1000, full = 4 * kCus * tile_bytes * (B > 1 ? 7 : 10) / 54000;
   int64_t least = 0, best = 1;
   for (int64_t k = 1; k <= 128 && (k == 1 || (4 * k < tiles + 4 && blocks * (k - 1) < 4 * kCus)); ++k) {
     const int64_t n = blocks * k, each = (n + kCus - 1) / kCus, steps = ((tiles + k - 1) / k + 3) / 4;
