@@ -86,6 +86,16 @@ __device__ __forceinline__ b4i widen_codes(int lo, int hi) {
   return r;
 }
 
+// what lane N of each row of 16 lanes holds
+template <int N>
+__device__ __forceinline__ float of_lane(float v) {
+  return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x150 + N, 0xF, 0xF, true));
+}
+template <class Fn, int... I>
+__device__ __forceinline__ void each(Fn&& fn, std::integer_sequence<int, I...>) {
+  (fn(std::integral_constant<int, I>{}), ...);
+}
+
 // over the four lanes of a row
 __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, __shfl_xor(v, 16));
@@ -203,42 +213,41 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
 
   // ---- loads of the tile at j
   b4i kw[NT][NC], vw[ND];
-  b4f ks[NT], vs[NT];
-  auto load_k = [&](int j, int page) __attribute__((always_inline)) {
-    const uint8_t* kp = static_cast<const uint8_t*>(c.k) +
-                        ES * (max(page, 0) * c.k_page + (((int64_t)h << p.shift) + ((j + kg + (lc & 3)) & mask)) * D) + 16 * lu;
+  float ks = 0.f, vs = 0.f;                      // scales of key KPL lu + lc
+  auto k_at = [&](int j, int page) __attribute__((always_inline)) -> const uint8_t* {
+    return static_cast<const uint8_t*>(c.k) +
+           ES * (max(page, 0) * c.k_page + (((int64_t)h << p.shift) + ((j + kg + (lc & 3)) & mask)) * D) + 16 * lu;
+  };
+  auto load_k = [&](const uint8_t* kp, int t) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        if (PAD) kw[t][i] = (b4i){0, 0, 0, 0};
-        if (!PAD || 64 * i + 16 * lu < ES * D) kw[t][i] = *reinterpret_cast<const b4i*>(kp + 4 * t * ES * D + 64 * i);
-      }
+    for (int i = 0; i < NC; ++i) {
+      if (PAD) kw[t][i] = (b4i){0, 0, 0, 0};
+      if (!PAD || 64 * i + 16 * lu < ES * D) kw[t][i] = *reinterpret_cast<const b4i*>(kp + 4 * t * ES * D + 64 * i);
+    }
   };
   auto load_scales = [&](int j, int page) __attribute__((always_inline)) {
     if constexpr (CODES) {
-      const int64_t at = max(page, 0) * c.scale_page + ((int64_t)h << p.shift) + ((j + vg) & mask);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        ks[t] = *reinterpret_cast<const b4f*>(c.k_scale + at + 4 * t);
-        vs[t] = *reinterpret_cast<const b4f*>(c.v_scale + at + 4 * t);
-      }
+      const int64_t at = max(page, 0) * c.scale_page + ((int64_t)h << p.shift) + ((j + vg) & mask) + lc;
+      ks = c.k_scale[at];
+      vs = c.v_scale[at];
     }
   };
-  auto load_v = [&](int j, int page) __attribute__((always_inline)) {
-    const uint8_t* vp = static_cast<const uint8_t*>(c.v) +
-                        ES * (max(page, 0) * c.v_page + (((int64_t)h * D + lc) << p.shift) + ((j + vg) & mask));
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      if (PAD) vw[d] = (b4i){0, 0, 0, 0};
-      if (!PAD || 16 * d < D) vw[d] = *reinterpret_cast<const b4i*>(vp + ((size_t)(16 * d * ES) << p.shift));
-    }
+  auto v_at = [&](int j, int page) __attribute__((always_inline)) -> const uint8_t* {
+    return static_cast<const uint8_t*>(c.v) +
+           ES * (max(page, 0) * c.v_page + (((int64_t)h * D + lc) << p.shift) + ((j + vg) & mask));
+  };
+  auto load_v = [&](const uint8_t* vp, int d) __attribute__((always_inline)) {
+    if (PAD) vw[d] = (b4i){0, 0, 0, 0};
+    if (!PAD || 16 * d < D) vw[d] = *reinterpret_cast<const b4i*>(vp + ((size_t)(16 * d * ES) << p.shift));
   };
 
   if (j < end) {
-    load_k(j, kpage);
+    const uint8_t *kp = k_at(j, kpage), *vp = v_at(j, vpage);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) load_k(kp, t);
     load_scales(j, vpage);
-    load_v(j, vpage);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) load_v(vp, d);
   }
 
   // ---- Q as the B operand, while the first tile is on its way
@@ -365,22 +374,25 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
         }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (MORE) load_k(j + STEP, knext);
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (CODES) {
-      if (cut) {
+    // The next tile's K in four places among this tile's softmax, its V among the products
+    // with V: a wave that asks for much at once waits until the unit has taken it in.
+    const uint8_t* kp = nullptr;
+    auto more_k = [&](int quarter) __attribute__((always_inline)) {
+      if constexpr (MORE) {
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int x = 0; x < KPL; ++x)
-          if (x < lo || x >= hi) vs[x / 4][x % 4] = 0.f;
+        for (int t = NT * quarter / 4; t < NT * (quarter + 1) / 4; ++t) load_k(kp, t);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    if constexpr (MORE) kp = k_at(j + STEP, knext);
+    more_k(0);
+    if constexpr (CODES) {
+      if (lc < lo || lc >= hi) vs = 0.f;
       // room for V's scales
-      float big = 0.f;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) big = fmaxf(big, vs[t][i]);
+      float big = vs;
       if (__any(big * iv > 1.0f)) {
-        big = row_max(big);
+        for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
         const int e = min(max((int)(__float_as_uint(big) >> 23) - 126, -126), 126);   // big < 2^e
         const float next = __uint_as_float((uint32_t)(127 - e) << 23);
         const float f = next * (1.0f / iv);   // (iv is a power of two: exact, or 0)
@@ -393,17 +405,14 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
         iv = next;
       }
     }
+    more_k(1);
     b4i pf[RT][NU];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       // in powers of two; rounded here and not in the exponent's sum, so that the largest
       // of enormous scores is the maximum itself
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if constexpr (CODES) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[r][t][i] = s[r][t][i] * ks[t][i] * rq[r];
-        }
+      if constexpr (CODES)
+        each([&](auto x) { s[r][x / 4][x % 4] = s[r][x / 4][x % 4] * of_lane<x>(ks) * rq[r]; }, std::make_integer_sequence<int, KPL>{});
       if (a.softcap > 0.f) {
         const PagedP p = again();
         if (p.a.softcap <= kSmallCap) {
@@ -438,6 +447,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
           for (int i = 0; i < 4; ++i)
             if (4 * t + i < lo || 4 * t + i >= hi) s[r][t][i] = -__builtin_inff();
       }
+      if (r == 0) more_k(2);
       float top = s[r][0][0];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
@@ -452,19 +462,23 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[r][d] *= f;
       }
+      if (r == 0) more_k(3);
+      float w[4 * NT];
+#pragma unroll
+      for (int x = 0; x < 4 * NT; ++x) {
+        w[x] = exp2_(s[r][x / 4][x % 4] - m[r]);
+        l[r] += w[x];
+      }
+      if constexpr (CODES) {
+        const float by = vs * iv;
+        each([&](auto x) { w[x] *= of_lane<x>(by); }, std::make_integer_sequence<int, KPL>{});
+      }
+      // To the product with V the weights go in 16 bits, as the matrix unit takes them
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = exp2_(s[r][t][i] - m[r]);
-          l[r] += w[i];
-          if constexpr (CODES) w[i] *= vs[t][i] * iv;
-        }
-        // To the product with V the weights go in 16 bits, as the matrix unit takes them
         constexpr int T16 = FP16 ? SVDQ_FP16 : SVDQ_BF16, I1 = INT8 ? 2 : 1, I2 = INT8 ? 1 : 2;   // in V's order
-        pf[r][t / 2][2 * (t % 2)] = (int)narrow2<T16>(w[0], w[I1]);
-        pf[r][t / 2][2 * (t % 2) + 1] = (int)narrow2<T16>(w[I2], w[3]);
+        pf[r][t / 2][2 * (t % 2)] = (int)narrow2<T16>(w[4 * t], w[4 * t + I1]);
+        pf[r][t / 2][2 * (t % 2) + 1] = (int)narrow2<T16>(w[4 * t + I2], w[4 * t + 3]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -486,16 +500,24 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
         for (int d = 0; d < ND; ++d) vw[d][i] &= (int)keep;
       }
     }
+    const uint8_t* vp = nullptr;
+    if constexpr (MORE) vp = v_at(j + STEP, vnext);
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int d = 0; d < ND; ++d) {
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
+      for (int u = 0; u < NU; ++u) {
         b4i vf;
         if constexpr (CODES) vf = widen_codes<FMT>(vw[d][2 * u], vw[d][2 * u + 1]);
         else vf = vw[d];
 #pragma unroll
         for (int r = 0; r < RT; ++r) o[r][d] = mma16<FP16>(vf, pf[r][u], o[r][d]);
       }
+      if constexpr (MORE) {
+        __builtin_amdgcn_sched_barrier(0);
+        load_v(vp, d);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     if constexpr (INT8) {
       // -128 2^-24 times the sum of the weights as rounded
       const int less = (int)0x80808080;
@@ -506,8 +528,6 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (MORE) {
-      load_v(j + STEP, vnext);
-      __builtin_amdgcn_sched_barrier(0);
       kpage = knext;
       vpage = vnext;
       knext = kafter;
