@@ -706,11 +706,19 @@ class KVCache:
     float8_e4m3fn codes with float32 k_scale, v_scale [pages, heads, page], or
     bfloat16, float16 or int16 (bf16 bits) values without.  A page's own elements
     are contiguous; pages may be any distance apart.  page: 16, 32, .. 256; D a
-    multiple of 16 up to 128.  The cache goes on using these tensors' memory."""
+    multiple of 16 up to 128.  The cache goes on using these tensors' memory: they
+    are not to be resized, and another tensor takes a new KVCache.  A copy has copies
+    of them."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.handle = (_blk or _block()).kv_cache(k, v, k_scale, v_scale)
+        self._tensors = k, v, k_scale, v_scale
+        self._handle = (_blk or _block()).kv_cache(*self._tensors)
+
+    k, v, k_scale, v_scale = (property(lambda self, i=i: self._tensors[i]) for i in range(4))
+    handle = property(lambda self: self._handle)    # addresses and sizes, as the calls take them
+
+    def __reduce__(self):
+        return KVCache, self._tensors
 
     @classmethod
     def empty(cls, pages, heads, head_dim, page=64, format="int8", device="cuda"):
