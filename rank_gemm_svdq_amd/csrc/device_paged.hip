@@ -27,6 +27,16 @@
 // Softmax.  A row's maximum is raised when a tile exceeds it by more than kLag
 // (powers of two), which a vote of the wave finds out without exchanges; weights
 // then carry 2^kLift to the middle of their type's range.
+//
+// What bounds it.  Each key and value is read once, and the memory's rate is reached where
+// all compute units have work: 16 requests of up to 16384 INT8 keys, 8 heads of 128,
+// 67.0 us; one of 131072 E4M3 keys 55.5; 40 of up to 3001 fp16 keys within a window of
+// 1500, 24 heads of 64, 63.5.  A compute unit by itself takes in 27 GB/s from memory and 46
+// from the last-level cache, however many waves ask, so fewer blocks than units leave the
+// rate behind; 600 INT8 keys take 9.1 us, which is two launches and the chain
+// length, page, K, scores, V, join.  (Blocks of eight waves, a
+// wave on two tiles at a time, K in whole lines with its pieces exchanged: the same time;
+// K and V loaded past the caches: 5 to 10 % more.)
 #include "device_kv.h"
 #include "device_score.h"
 
@@ -319,7 +329,6 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
   // operands is asked for as soon as this tile's has been used, into the same registers.
   auto tile = [&](int j, auto more) __attribute__((always_inline)) {
     constexpr bool MORE = decltype(more)::value;
-    
     const int vj = j + vg;
     // keys [lo, hi) of the lane's are visible
     const int lo = vpage >= 0 ? sn.lo - vj : KPL, hi = vpage >= 0 ? end - vj : 0;
@@ -646,16 +655,18 @@ struct PagedPlan {
   int G, rows, share, splits;
 };
 // Parts of a row of keys by the least time, in ns.  A compute unit brings in what the four
-// tiles of a block's step need in 2000 (heads of 128; 1600 from the last-level cache, 2400
-// from memory; what it can have under way at a time bounds it, and a second block
-// beside the first does not help), or all of them at the rate of the memory, of which a
-// batch's lengths leave about 0.7 in use; so blocks are as many to a compute unit as the
-// fullest has.  Start and end are 4500, 700 more for each block after the first, and the
-// join 2500, 100 a part up to 16 and 8 a part.
-// (us for 1, 2, 4, 8 .. parts: 4096 keys x 8 heads 28.5, 19.1, 13.1, 11.3, 10.3;
-// 131072 x 8 in 16, 32, 48, 64 parts 82.7, 55.8, 66.2, 57.2; 16 requests of up to 16384 in
-// 1, 2, 3, 4: 111, 79, 95, 80; 64 of 1024 20.4, 26.0, 33.4; 40 of 4096 64.9, 60.1, 58.6, 62.5.
-// Eight waves a block took the same time at as many blocks.)
+// tiles of a block's step need (heads of 128) in 1490 where few blocks run, 2090 where 128
+// do (what it can have under way at a time bounds it, and a second block beside the first
+// does not help), or all of them at the rate of the memory, of which a batch's
+// lengths leave about 0.7 in use; so blocks are as many to a compute unit as the fullest
+// has.  Start and end are 4500, 700 more for each block after the first, and the join
+// 3900, 100 a part up to 16 and 8 a part.
+// (us in 1, 2, 4, 8, 16, 32 parts, 8 K/V heads of 128, codes: 640 keys 9.9, 11.9, 10.8 from
+// memory and 8.2, 10.0, 9.1 from the last-level cache; 4096 keys 24.6, 17.2, 12.3, 11.0,
+// 10.5, 10.5; 16384 88, 49, 28.6, 18.8, 14.5, 13.7; 131072 984, 501, 258, 137, 78, 55.3, in 48
+// 65.5; 16 requests of up to 16384 in 1, 2, 3, 4 97.7, 67.0, 84.0, 70.0; 64 of 1024 18.9, 24.5,
+// 24.4; 40 of 4096 58.3, 53.7, 55.1, 52.2.  A dearer join costs single long requests, a
+// cheaper one batches of some hundred keys: 16 of 1280 14.4 in one part, 16.2 in two.)
 PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   PagedPlan p;
   p.G = Hq / c.heads;
@@ -663,12 +674,13 @@ PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   const int64_t blocks = (int64_t)B * c.heads * p.rows;
   const int64_t tile_keys = c.format == SVDQ_KV_VALUES ? 32 : 64, tile_bytes = 128 * padded_dim(c.D) + 512;
   const int64_t tiles = (keys + tile_keys - 1) / tile_keys;
-  const int64_t alone = 250 + tile_bytes * 104 / 1000, full = 4 * kCus * tile_bytes * (B > 1 ? 7 : 10) / 54000;
+  const int64_t full = 4 * kCus * tile_bytes * (B > 1 ? 7 : 10) / 54000;
   int64_t least = 0, best = 1;
   for (int64_t k = 1; k <= 128 && (k == 1 || (4 * k < tiles + 4 && blocks * (k - 1) < 4 * kCus)); ++k) {
     const int64_t n = blocks * k, each = (n + kCus - 1) / kCus, steps = ((tiles + k - 1) / k + 3) / 4;
+    const int64_t alone = 250 + tile_bytes * 71 / 1000 + tile_bytes * (n < 128 ? n : 128) / 3400;
     const int64_t step = n >= kCus ? full : full * n / kCus;
-    const int64_t cost = each * (steps * (step > alone ? step : alone) + 700) + 3800 + (k > 1 ? 2500 + 100 * (k < 16 ? k : 16) + 8 * k : 0);
+    const int64_t cost = each * (steps * (step > alone ? step : alone) + 700) + 3800 + (k > 1 ? 3900 + 100 * (k < 16 ? k : 16) + 8 * k : 0);
     if (k == 1 || cost < least) {
       least = cost;
       best = k;
