@@ -539,7 +539,7 @@ typedef struct svdq_kv_cache {
 } svdq_kv_cache;
 
 typedef struct svdq_cache_write_args {
-  int32_t M;                    /* tokens, 1..2^20; ceil(M / 16) heads < 2^24 */
+  int32_t M;                    /* tokens, 1..2^20; ceil((M + 7) / 64) heads < 2^24 */
   int32_t B, T;                 /* the table: requests and pages of each, B >= 1, 1 <= T, T page <= 2^24 */
   int32_t dtype;
   const int32_t* table;         /* device, row b at b * table_row */
@@ -584,7 +584,7 @@ typedef struct svdq_paged_attention_args {
   float scale;                  /* of q . k */
   float softcap;                /* > 0: scores become softcap * tanh(score / softcap); 0: off */
   const uint16_t* q;            /* device, element (b, h, d) at b * batch + h * head + d; multiples of 8 elements */
-  uint16_t* o;
+  uint16_t* o;                  /* overlaps no operand */
   int64_t q_batch, q_head, o_batch, o_head;
   const int32_t* table;
   int64_t table_row;

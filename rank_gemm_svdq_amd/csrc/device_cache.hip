@@ -4,8 +4,15 @@
 // Keys lie token by token, [page][head][place][D], and values element by element,
 // [page][head][D][place], so that attention's matrix operands are 16-byte loads of
 // either (device_paged.hip).  Values therefore turn on their way through LDS: a
-// block takes a run of tokens of one head, and rows of it that lie side by side in a
-// page are stored four tokens at a time, others one by one.
+// block takes 64 tokens of one head, and eights of them that lie side by side in a
+// page from a place that is a multiple of 8 are stored and loaded as one piece (four at
+// a time 22.0 us for what takes 18.2 now), others one by one.  Few tokens go
+// straight from registers (write_few_kernel).
+//
+// Both ways move each value once and each code once, and the memory's rate bounds
+// them: 4608 tokens x 24 heads of 128 into E4M3 codes 18.2 us, out of them 17.8 us, 4.7
+// and 4.8 TB/s.  (What is read back stored past the caches: the attention that reads it
+// loses more.)
 //
 // Codes.  INT8: s = max (1 / 127), the code nearest to x / s.  The first guess
 // rint(x / s) by a reciprocal is off by at most one, and x - code s, which one fma
@@ -17,8 +24,8 @@
 namespace svdq {
 namespace {
 
-// Sizes of a cache's elements and lanes: LPR lanes (8 elements each) hold a token's
-// vector; a dword of a row in LDS holds QD elements.
+// LPR lanes (8 elements each) hold a token's vector.  A value or code has ES bytes; a
+// dword of a row in LDS holds QD elements.
 template <int FMT, int LPR>
 struct CacheShape {
   static constexpr int ES = FMT == SVDQ_KV_VALUES ? 2 : 1;
@@ -410,9 +417,9 @@ extern "C" svdq_status svdq_cache_write(const svdq_kv_cache* cache, const svdq_c
   if (!is_dtype(a.dtype)) return SVDQ_ERR_UNSUPPORTED;
   if (!table_fits(*cache, a.B, a.T, a.table_row)) return SVDQ_ERR_SHAPE;
   if (a.M < 1 || a.M > (1 << 20) || (!a.entry && a.M > a.B)) return SVDQ_ERR_SHAPE;
-  // Blocks of 64 tokens and a head, or where they are few, 16 or 32 lots of one token and
-  // head (a run of 512 tokens x 8 heads of 128 7.3 -> 5.9 us, 1024 7.8 -> 8.9; 16 requests' next
-  // tokens 6.4 -> 3.9, 128 requests' 9.5 -> 4.9).
+  // Blocks of 64 tokens and a head, or where those are few, 16 or 32 lots of one token and
+  // one head (a run of 512 tokens x 8 heads of 128 5.9 us instead of 7.3, of 1024 8.9 instead of
+  // 7.8; the next tokens of 16 requests 3.9 instead of 6.4, of 128 4.9 instead of 9.5).
   const bool few = (int64_t)((a.M + 63) / 64) * cache->heads < 128;
   const int lots = cache->D <= 64 ? 32 : 16;
   const int64_t blocks = few ? ((int64_t)a.M * cache->heads + lots - 1) / lots : (int64_t)((a.M + 7 + 63) / 64) * cache->heads;

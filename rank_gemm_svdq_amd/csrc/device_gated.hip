@@ -87,14 +87,14 @@ __global__ __launch_bounds__(1024) void gated_kernel(svdq_gated_norm_args a, int
     off = 0.f;
     if (kind == SVDQ_NORM_NONE) return;
     float mean = 0.f;
-    auto square = [&](float by, float eps) __attribute__((always_inline)) -> float {   // mean square of (v - mean) by, and eps
+    auto square = [&](float eps) __attribute__((always_inline)) -> float {   // mean square of v - mean, and eps
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float d = (v[c][i] - mean) * by;
+          const float d = v[c][i] - mean;
           s = fmaf(d, d, s);
         }
         sum += first + c * stride < chunks ? s : 0.f;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(1024) void gated_kernel(svdq_gated_norm_args a, int
       mean = total(sum) / (float)a.K;
     };
     centre();
-    float var = square(1.f, a.eps);
+    float var = square(a.eps);
     if (__builtin_expect(!(var >= 0x1p-80f && var < __builtin_inff()), 0)) {
       // the deviations themselves, as v
       float by = 0x1p90f;
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(1024) void gated_kernel(svdq_gated_norm_args a, int
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[c][i] = first + c * stride < chunks ? (v[c][i] - mean) * up : 0.f;
       mean = 0.f;
-      var = square(1.f, a.eps * by * by);
+      var = square(a.eps * by * by);
     }
     inv = 1.0f / sqrtf(var);
     off = -mean * inv;
