@@ -30,7 +30,7 @@
 //
 // What bounds it.  Each key and value is read once, and the memory's rate is reached where
 // all compute units have work: 16 requests of up to 16384 INT8 keys, 8 heads of 128,
-// 67.0 us; one of 131072 E4M3 keys 55.5; 40 of up to 3001 fp16 keys within a window of
+// 66.7 us; one of 131072 E4M3 keys 54.1; 40 of up to 3001 fp16 keys within a window of
 // 1500, 24 heads of 64, 63.5.  A compute unit by itself takes in 27 GB/s from memory and 46
 // from the last-level cache, however many waves ask, so fewer blocks than units leave the
 // rate behind; 600 INT8 keys take 9.1 us, which is two launches and the chain
@@ -593,44 +593,77 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
 }
 
 // Joins the parts of the rows: DP / 8 lanes hold a row's 8-element pieces, and
-// `across` such lane sets (1, 2, .. 16) of a block share the row's parts.
+// `across` such lane sets (1, 2, .. 16) of a block share the row's parts, two at a time.
+// The sets of a wave are joined by exchanges and the waves through LDS (every set's sums
+// through LDS in turn: 1.1 us more for 32 parts, 0.9 for 16).
 template <int DT, int DP>
 __global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
   const svdq_paged_attention_args& a = p.a;
   constexpr int LPR = DP / 8;
-  __shared__ float part[256][11];   // 8 sums, maximum, sum of weights; 11: odd stride
+  __shared__ float part[4][LPR][11];   // of a wave: 8 sums, maximum, sum of weights; 11: odd stride
   const size_t rows = (size_t)a.B * a.Hq;
-  const int set = threadIdx.x / LPR, g = set % across, d = 8 * (threadIdx.x % LPR);
+  const int set = threadIdx.x / LPR, g = set % across, lane = threadIdx.x % LPR, d = 8 * lane;
   const size_t at = (size_t)blockIdx.x * (256 / LPR / across) + set / across;
   const bool live = at < rows;
   float top = kLow, sum = 0.f, o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
   if (live) {
-    for (int s = g; s < p.part.splits; s += across) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part.ml + 2 * (s * rows + at));
-      const float* op = p.part.o + (s * rows + at) * DP + d;
-      const b4f x = *reinterpret_cast<const b4f*>(op), y = *reinterpret_cast<const b4f*>(op + 4);
-      if (ml.y == 0.f) continue;                 // no keys, and nothing stored; or no weights
-      const float up = fmaxf(top, ml.x), f0 = exp2_(top - up), f = ml.y * exp2_(ml.x - up);
-      sum = fmaf(sum, f0, f);
+    for (int s = g; s < p.part.splits; s += 2 * across) {
+      float2 ml[2] = {};
+      b4f x[2][2] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[i] = fmaf(f, x[i], o[i] * f0);
-        o[4 + i] = fmaf(f, y[i], o[4 + i] * f0);
+      for (int k = 0; k < 2; ++k) {
+        if (k == 1 && p.part.splits <= across) break;   // one part a set
+        const size_t pt = min(s + k * across, p.part.splits - 1) * rows + at;
+        const float* op = p.part.o + pt * DP + d;
+        ml[k] = *reinterpret_cast<const float2*>(p.part.ml + 2 * pt);
+        x[k][0] = *reinterpret_cast<const b4f*>(op);
+        x[k][1] = *reinterpret_cast<const b4f*>(op + 4);
       }
-      top = up;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // no keys, and nothing stored; or no weights
+        if (s + k * across >= p.part.splits || ml[k].y == 0.f) continue;
+        const float up = fmaxf(top, ml[k].x), f0 = exp2_(top - up), f = ml[k].y * exp2_(ml[k].x - up);
+        sum = fmaf(sum, f0, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(f, x[k][i / 4][i % 4], o[i] * f0);
+        top = up;
+      }
     }
   }
+  // the sets of a wave
   if (across > 1) {
+    float up = top;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = o[i];
-    part[threadIdx.x][8] = top;
-    part[threadIdx.x][9] = sum;
+    for (int w = LPR; w < 64; w *= 2)
+      if (w < across * LPR) up = fmaxf(up, __shfl_xor(up, w));
+    const float f = exp2_(top - up);
+    top = up;
+    sum *= f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= f;
+#pragma unroll
+    for (int w = LPR; w < 64; w *= 2)
+      if (w < across * LPR) {
+        sum += __shfl_xor(sum, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += __shfl_xor(o[i], w);
+      }
+  }
+  if (across * LPR > 64) {
+    const int wave = threadIdx.x >> 6, waves = across * LPR / 64;
+    if ((threadIdx.x & 63) < LPR) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) part[wave][lane][i] = o[i];
+      part[wave][lane][8] = top;
+      part[wave][lane][9] = sum;
+    }
     __syncthreads();
     if (g == 0) {
-      for (int k = 1; k < across; ++k) {
-        const float* x = part[threadIdx.x + k * LPR];
+      for (int k = 1; k < waves; ++k) {
+        const float* x = part[wave + k][lane];
         const float up = fmaxf(top, x[8]), f0 = exp2_(top - up), f = exp2_(x[8] - up);
         sum = fmaf(f, x[9], sum * f0);
 #pragma unroll
@@ -661,12 +694,12 @@ struct PagedPlan {
 // lengths leave about 0.7 in use; so blocks are as many to a compute unit as the fullest
 // has.  Start and end are 4500, 700 more for each block after the first, and the join
 // 3900, 100 a part up to 16 and 8 a part.
-// (us in 1, 2, 4, 8, 16, 32 parts, 8 K/V heads of 128, codes: 640 keys 9.9, 11.9, 10.8 from
-// memory and 8.2, 10.0, 9.1 from the last-level cache; 4096 keys 24.6, 17.2, 12.3, 11.0,
-// 10.5, 10.5; 16384 88, 49, 28.6, 18.8, 14.5, 13.7; 131072 984, 501, 258, 137, 78, 55.3, in 48
-// 65.5; 16 requests of up to 16384 in 1, 2, 3, 4 97.7, 67.0, 84.0, 70.0; 64 of 1024 18.9, 24.5,
-// 24.4; 40 of 4096 58.3, 53.7, 55.1, 52.2.  A dearer join costs single long requests, a
-// cheaper one batches of some hundred keys: 16 of 1280 14.4 in one part, 16.2 in two.)
+// (us in 1, 2, 4, 8, 16, 32 parts, 8 K/V heads of 128, codes: 640 keys 9.9, 11.8, 11.3 from
+// memory and 8.3, 9.9, 9.0 from the last-level cache; 4096 keys 24.8, 16.9, 12.3, 11.0,
+// 9.9, 9.8; 16384 88, 49, 28.6, 18.4, 13.9, 12.9; 131072 986, 501, 258, 137, 78, 54.1, in 48
+// 64.2; 16 requests of up to 16384 in 1, 2, 3, 4 98.1, 67.0, 83.7, 69.9; 64 of 1024 19.0, 24.6,
+// 24.6; 40 of 4096 58.2, 53.6, 55.2, 52.5.  A dearer join costs single long requests, a
+// cheaper one batches of some hundred keys: 16 of 1280 14.7 in one part, 16.1 in two.)
 PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   PagedPlan p;
   p.G = Hq / c.heads;
