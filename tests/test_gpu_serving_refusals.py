@@ -173,3 +173,39 @@ def test_a_cache_keeps_its_memory():
         assert torch.equal(attend(cache), want) and attend(other).isnan().all()
     shallow = copy.copy(cache)
     assert shallow.k is cache.k and torch.equal(attend(shallow), want)
+
+
+def test_bits_of_bf16_are_bf16():
+    """int16 tensors stand for the bits of bf16 ones, the cache's too."""
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn((20, HEADS, D), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn((1, 4, D), generator=g).to(torch.bfloat16).cuda()
+    table, bits = ints([[3, 1]]), lambda t: t.view(torch.int16)
+    got = []
+    for view in (lambda t: t, bits):
+        cache = B.KVCache(view(bf16(PAGES, HEADS, PAGE, D)), view(bf16(PAGES, HEADS, D, PAGE)))
+        B.cache_write(cache, table, ints(range(20)), view(k), view(v), entry=ints([0] * 20))
+        o, kr, vr = torch.empty_like(q), bf16(1, 20, HEADS, D), bf16(1, 20, HEADS, D)
+        B.paged_attention(view(q), cache, table, ints([20]), view(o), B.paged_attention_workspace(q, cache, table))
+        B.cache_read(cache, table, ints([20]), view(kr), view(vr))
+        assert torch.equal(kr[0], k) and torch.equal(vr[0], v)
+        got.append(o)
+    assert got[0].float().abs().sum() > 0 and torch.equal(got[0], got[1])
+
+
+def test_writes_of_two_streams_into_one_page():
+    """Calls that overlap in time may write different places of the same page."""
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn((64, 40, 64), generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    table = ints([[2]])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for fmt in ("int8", "bf16"):
+        whole, parts = (B.KVCache.empty(3, 40, 64, page=64, format=fmt) for _ in range(2))
+        B.cache_write(whole, table, ints(range(64)), k, v, entry=ints([0] * 64))
+        places = [ints(range(0, 29)), ints(range(29, 64))]
+        entries = [ints([0] * 29), ints([0] * 35)]
+        torch.cuda.synchronize()
+        for s, at, e, lo, hi in zip(streams, places, entries, (0, 29), (29, 64)):
+            B.cache_write(parts, table, at, k[lo:hi], v[lo:hi], entry=e, stream=s)
+        torch.cuda.synchronize()
+        assert torch.equal(parts.k, whole.k) and torch.equal(parts.v, whole.v) and whole.v.float().abs().sum() > 0
