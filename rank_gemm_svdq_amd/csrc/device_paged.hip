@@ -568,17 +568,16 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
   for (int i = threadIdx.x; i < 16 * RT * (DP / 4); i += 64 * NW) {
     const int r = i / (DP / 4), d = 4 * (i % (DP / 4)), row = rb * 16 * RT + r;
     if (row >= e.G || d >= D) continue;
-    float up = jm[0][r][0], sum = 0.f;
+    float up = jm[0][r][0], sum = 0.f, f[NW];
 #pragma unroll
     for (int w = 1; w < NW; ++w) up = fmaxf(up, jm[w][r][0]);
+#pragma unroll
+    for (int w = 0; w < NW; ++w) sum += f[w] = jm[w][r][1] * exp2_(jm[w][r][0] - up);
+    // shares of the sum, not weights: a mean near the type's largest value times a weight leaves fp32
+    const float by = sum != 0.f ? 1.0f / sum : 0.f;
     b4f x = (b4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float f = jm[w][r][1] * exp2_(jm[w][r][0] - up);
-      sum += f;
-      x += *reinterpret_cast<const b4f*>(&jo[w][r][d]) * f;
-    }
-    x *= sum != 0.f ? 1.0f / sum : 0.f;
+    for (int w = 0; w < NW; ++w) x += *reinterpret_cast<const b4f*>(&jo[w][r][d]) * (f[w] * by);
     const size_t at = (size_t)b * e.a.Hq + h * e.G + row;
     if (e.part.splits > 1) {
       const size_t pt = (size_t)sp * ((size_t)a.B * e.a.Hq) + at;
@@ -600,14 +599,24 @@ template <int DT, int DP>
 __global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
   const svdq_paged_attention_args& a = p.a;
   constexpr int LPR = DP / 8;
-  __shared__ float part[4][LPR][11];   // of a wave: 8 sums, maximum, sum of weights; 11: odd stride
+  __shared__ float part[4][LPR][11];   // of a wave: 8 means, maximum, sum of weights; 11: odd stride
   const size_t rows = (size_t)a.B * a.Hq;
   const int set = threadIdx.x / LPR, g = set % across, lane = threadIdx.x % LPR, d = 8 * lane;
   const size_t at = (size_t)blockIdx.x * (256 / LPR / across) + set / across;
   const bool live = at < rows;
-  float top = kLow, sum = 0.f, o[8];
+  float top = kLow, sum = 0.f, o[8];             // o: the mean so far
 #pragma unroll
   for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  // The mean x of weights of sum f under maximum m joins this set's, each times its share
+  // of the sum: a mean near the type's largest value times a weight leaves fp32.
+  auto add = [&](float m, float f, const float* x) __attribute__((always_inline)) {
+    const float up = fmaxf(top, m), mine = sum * exp2_(top - up), other = f * exp2_(m - up);
+    top = up;
+    sum = mine + other;
+    const float by = sum != 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f, b = other * by;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(b, x[i], o[i] * (mine * by));
+  };
   if (live) {
     for (int s = g; s < p.part.splits; s += 2 * across) {
       float2 ml[2] = {};
@@ -625,11 +634,8 @@ __global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
       for (int k = 0; k < 2; ++k) {
         // no keys, and nothing stored; or no weights
         if (s + k * across >= p.part.splits || ml[k].y == 0.f) continue;
-        const float up = fmaxf(top, ml[k].x), f0 = exp2_(top - up), f = ml[k].y * exp2_(ml[k].x - up);
-        sum = fmaf(sum, f0, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(f, x[k][i / 4][i % 4], o[i] * f0);
-        top = up;
+        const float t[8] = {x[k][0][0], x[k][0][1], x[k][0][2], x[k][0][3], x[k][1][0], x[k][1][1], x[k][1][2], x[k][1][3]};
+        add(ml[k].x, ml[k].y, t);
       }
     }
   }
@@ -639,18 +645,20 @@ __global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
 #pragma unroll
     for (int w = LPR; w < 64; w *= 2)
       if (w < across * LPR) up = fmaxf(up, __shfl_xor(up, w));
-    const float f = exp2_(top - up);
+    const float mine = sum * exp2_(top - up);
     top = up;
-    sum *= f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= f;
+    sum = mine;
 #pragma unroll
     for (int w = LPR; w < 64; w *= 2)
-      if (w < across * LPR) {
-        sum += __shfl_xor(sum, w);
+      if (w < across * LPR) sum += __shfl_xor(sum, w);
+    const float share = sum != 0.f ? mine * __builtin_amdgcn_rcpf(sum) : 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += __shfl_xor(o[i], w);
-      }
+    for (int i = 0; i < 8; ++i) {
+      o[i] *= share;
+#pragma unroll
+      for (int w = LPR; w < 64; w *= 2)
+        if (w < across * LPR) o[i] += __shfl_xor(o[i], w);
+    }
   }
   if (across * LPR > 64) {
     const int wave = threadIdx.x >> 6, waves = across * LPR / 64;
@@ -661,21 +669,10 @@ __global__ __launch_bounds__(256) void paged_join(PagedP p, int across) {
       part[wave][lane][9] = sum;
     }
     __syncthreads();
-    if (g == 0) {
-      for (int k = 1; k < waves; ++k) {
-        const float* x = part[wave + k][lane];
-        const float up = fmaxf(top, x[8]), f0 = exp2_(top - up), f = exp2_(x[8] - up);
-        sum = fmaf(f, x[9], sum * f0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(f, x[i], o[i] * f0);
-        top = up;
-      }
-    }
+    if (g == 0)
+      for (int k = 1; k < waves; ++k) add(part[wave + k][lane][8], part[wave + k][lane][9], part[wave + k][lane]);
   }
   if (!live || g != 0 || d >= p.c.D) return;
-  const float by = sum != 0.f ? 1.0f / sum : 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] *= by;
   const int b = (int)(at / a.Hq), hq = (int)(at % a.Hq);
   *reinterpret_cast<b4i*>(a.o + b * a.o_batch + hq * a.o_head + d) = narrow8<DT>(o);
   if (d == 0 && a.lse) a.lse[at] = sum != 0.f ? (top + __log2f(sum)) * 0.693147181f : -__builtin_inff();

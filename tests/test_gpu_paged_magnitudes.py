@@ -1,0 +1,82 @@
+"""Attention over 8-bit pages where scales, queries and values are of very different size, against the 64-bit oracle.
+
+Bound.  With u = 2^-24, p a key's weight of sum 1, V its largest |v| and n the keys seen:
+  score   (2 D + 16) u times its magnitudes, and what the query loses: E4M3 2^-25 of the row's largest element (half of
+          fp16's smallest step at [1, 2)), INT8 half a step of 2^-22 of a power of two that the largest is at least
+          0.996 of, 2^-22.9 of the largest, each times sum |k|;
+  weight  e^2d - 1 < 3 d relative, d that error and 2^-21 for the exponential, on mean |v| + |o|;
+  to fp16 2^-11 of each term, and 2^-25 absolute where the largest product p V / (127 or 224) is held above 2^6: 2^-31
+          of it a key, times codes of at most 127 or 448: n 2^-30 max (p V);
+  sums    (2 n + 16) u of mean |v| + |o|; INT8 values are summed as code + 128 <= 255 and 128 times the weights taken out:
+          2 n u of at most 3 sum p V.
+The store adds half an ulp.  The logarithm of the sum is off by d + 2 n u, 2^-17 and 2^-22 of itself."""
+import numpy as np
+import pytest
+import torch
+
+import rank_gemm_svdq_amd as B
+from oracle import serving as S
+from tests.block_util import assert_within, device, half_ulp, values
+from tests.serving_util import ints, numpy_of, random_cache, random_table
+
+pytestmark = pytest.mark.gpu
+U = 2.0**-24
+
+
+def _gpu(q, cache, table, kv_len, **kw):
+    o = torch.full(q.shape, float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    t = ints(table)
+    B.paged_attention(q, cache, t, ints(kv_len), o, B.paged_attention_workspace(q, cache, t), lse=lse, **kw)
+    torch.cuda.synchronize()
+    return o, lse
+
+
+def _bounds(qv, nc, table, kv_len, fmt, scale, exact=False):
+    """(o, its bound before the store, log sum, its bound); exact: queries whose elements are multiples of those steps"""
+    D = qv.shape[-1]
+    want, mean, weight, seen, ls = S.paged_attention(qv, nc, table, kv_len, scale)
+    k, v, _ = S.dense(nc, table)
+    G = qv.shape[1] // k.shape[2]
+    most, total = np.zeros(qv.shape[:2]), np.zeros(qv.shape[:2])      # max and sum of p V
+    for b in range(qv.shape[0]):
+        for h in range(qv.shape[1]):
+            z = scale * (k[b, :kv_len[b], h // G] @ qv[b, h])
+            pv = np.exp(z - ls[b, h]) * np.abs(v[b, :kv_len[b], h // G]).max(-1)
+            most[b, h], total[b, h] = pv.max(), pv.sum()
+    lost = 0.0 if exact else 2.0**-22.9 if fmt == "int8" else 2.0**-25
+    d = (2 * D + 16) * U * weight + 2.0**-21 + lost * np.abs(qv).max(-1) * abs(scale) * np.abs(k).sum(-1).max()
+    n = seen[..., None]
+    e = (3 * d[..., None] + 2.0**-11 + (2 * n + 16) * U) * (mean + np.abs(want)) + n * 2.0**-30 * most[..., None]
+    if fmt == "int8":
+        e = e + 6 * n * U * total[..., None]
+    return want, e, ls, d + 2 * seen * U + 2.0**-17 + 2.0**-22 * np.abs(ls)
+
+
+def _check(o, lse, qv, cache, table, kv_len, fmt, kind, scale, what, exact=False):
+    want, e, ls, off = _bounds(qv, numpy_of(cache), table, kv_len, fmt, scale, exact)
+    assert_within(values(o), want, e + half_ulp(np.abs(want) + e, kind), what)
+    assert_within(values(lse), ls, off, what + " lse")
+
+
+@pytest.mark.parametrize("fmt", ["fp8"])
+@pytest.mark.parametrize("low,high", [(2.0**103, 2.0**103), (2.0**118, 2.0**118), (2.0**90, 2.0**119), (2.0**-100, 2.0**119)])
+@pytest.mark.parametrize("order", [1, -1])
+def test_values_near_the_end_of_the_type(fmt, low, high, order):
+    """bf16 values of up to 1e38, some elements zero in all of them; in fp16 they are infinite."""
+    D, page, T = 64, 16, 20
+    for kind in ("bf16", "fp16"):
+        cache = random_cache(T, 2, page, D, fmt, kind, 201)
+        cache.v.view(torch.uint8)[:, :, 5:9] = 0
+        s = np.geomspace(low, high, T * page)[::order] * 127 / 448
+        cache.v_scale.copy_(torch.from_numpy(s.astype(np.float32)).view(T, 1, page).expand(T, 2, page))
+        table = np.arange(T)[None].astype(np.int32)
+        q, qv = device(0.3 * np.random.default_rng(202).standard_normal((1, 4, D)), kind)
+        o, lse = _gpu(q, cache, table, [T * page])
+        if kind == "bf16":
+            _check(o, lse, qv, cache, table, [T * page], fmt, kind, D ** -0.5, f"{low} {high}")
+        else:
+            want, e, _, _ = _bounds(qv, numpy_of(cache), table, [T * page], fmt, D ** -0.5)
+            got = values(o)
+            assert not np.isnan(got).any() and np.isinf(got[np.abs(want) - e >= 65520]).all()
+            assert (got[want == 0] == 0).all()
