@@ -552,8 +552,9 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     const float sum = row_sum(l[r]);
-    // a mean of codes is at most 448, so the scale comes back after the division
-    const float by = sum != 0.f ? 1.0f / sum : 0.f, back = CODES ? (INT8 ? 0x1p24f : 1.0f) / iv : 1.f;
+    // a mean of codes is at most 448, so the scale comes back after the division; INT8's
+    // 2^24 with the division, as together with the scale it may leave fp32
+    const float by = sum != 0.f ? (INT8 ? 0x1p24f : 1.0f) / sum : 0.f, back = CODES ? 1.0f / iv : 1.f;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
       *reinterpret_cast<b4f*>(&jo[wave][16 * r + lc][16 * d + 4 * lu]) =
