@@ -600,9 +600,10 @@ typedef struct svdq_paged_attention_args {
  * (infinities and NaN too) does not reach the output; a visible key's NaN makes
  * its rows NaN, a value's its element (all of them where its s is NaN).  Scores, the
  * running maximum and sum and O are fp32.  For the matrix unit queries are rounded to
- * 16 bits of their row's largest magnitude (SVDQ_KV_INT8) or to fp16 scaled by a power
- * of two (SVDQ_KV_FP8); with either a query that holds an infinity or a NaN gets NaN
- * where it sees a key.  Weights are rounded to fp16 (SVDQ_KV_VALUES: to the call's
+ * 24 bits, the sign's with them, of their row's largest magnitude (SVDQ_KV_INT8: an
+ * element is off by 2^-22.9 of it at most) or to fp16 scaled by a power of two
+ * (SVDQ_KV_FP8: by 2^-25 of it); with either a query that holds an infinity or a NaN
+ * gets NaN where it sees a key.  Weights are rounded to fp16 (SVDQ_KV_VALUES: to the call's
  * type) for the product with V, not for their sum.  The same call on the same inputs
  * gives the same bits.
  * ws: device, 256-byte aligned, svdq_paged_attention_workspace_bytes() bytes, or

@@ -19,7 +19,7 @@
 //
 // Codes.  E4M3 goes to fp16, exactly, and a query row with it, scaled by a power of two
 // that brings its largest element to [1, 2): what falls below fp16's range is under
-// 2^-24 of that.  INT8 keys are multiplied as they are by queries of 16 bits in two parts
+// 2^-24 of that.  INT8 keys are multiplied as they are by queries of 24 bits in three digits
 // of 8, summed exactly in int32; INT8 values become fp16 of their bits (widen_codes).
 // The key's scale multiplies the score, and the value's scale the weight, as a multiple
 // of a power of two that all the wave's scales so far stay under.
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
   constexpr int KPL = 16 / ES, TK = 4 * KPL;     // keys of a lane and of a tile
   constexpr int NT = TK / 16;                    // score tiles
   constexpr int NC = DP * ES / 64;               // 16-byte pieces of K a lane reads of a key
-  constexpr int NS = DP / 32;                    // MFMA steps of a score tile (INT8: as many, 64 wide, of two parts of Q)
+  constexpr int NS = DP / 32;                    // MFMA steps of a score tile (INT8: 3 NC, 64 wide, of three digits of Q)
   constexpr int ND = DP / 16;                    // element tiles of O
   constexpr int NU = TK / 32;                    // MFMA steps of O
   constexpr int NW = 4, STEP = NW * TK;          // waves, and keys from a wave's tile to its next
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
   const int b = entry, h = grp - entry * c.heads;
   const int D = PAD ? c.D : DP;
   // ---- Q: asked for before all else
-  b4i qf[RT][NS];
+  b4i qf[RT][NS], q8[RT][INT8 ? 3 * NC : 1];     // (q8: INT8's digits)
   float rq[RT], slope[RT];                       // a row's factor
   int qh[RT];
 #pragma unroll
@@ -280,28 +280,29 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
       const float mag = widen2<DT>((uint32_t)tb)[0];
       const bool odd = tb >= (DT == SVDQ_BF16 ? 0x7F80 : 0x7C00);
       if constexpr (INT8) {
-        // x 32512 / top, rounded, as 256 times one 8-bit part and another: 0.5 in 32512 is
-        // off, a 250th of what K's own codes are off by; the sums of products are exact.
-        // Adding 1.5 2^23 + 128 rounds, and leaves the first part in byte 1 and the other,
-        // 128 more, in byte 0.
-        const float by = mag > 0.f ? fminf(32512.0f / mag, 0x1p126f) * p.qmul : 0.f;
-        rq[r] = odd ? __builtin_nanf("") : fmaxf(mag * (1.0f / 32512.0f), 0x1p-126f);
+        // Whole numbers of 24 bits, in units of 2^-22 of a power of two that the largest element
+        // is between 0.996 and 1.992 of, as three signed digits of 8 bits: a bf16 element above
+        // 2^-15 of the largest keeps all its bits, and the sums of products are exact.  (Two
+        // digits: the output 0.2 to 2.5 % off where a channel of the query is 300 to 3000 times
+        // the others and the keys' is small in proportion; 600 keys 8.0 us, not 8.2.)
+        const int e = max((int)((__float_as_uint(mag) + 0x10000u) >> 23), 1) - 127;
+        rq[r] = odd ? __builtin_nanf("") : ldexpf(p.qmul, e - 22);
+        const int keep = odd ? 0 : -1;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-          b4i parts[2];
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const b4i& q4 = qf[r][2 * i + w / 2];
-            uint32_t v[4];
+            uint32_t v[4];                         // 128 more in each digit
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              v[k] = __float_as_uint(fmaf(widen2<DT>((uint32_t)q4[2 * (w % 2) + k / 2])[k % 2], by, 0x1.8p23f + 128.0f));
+              v[k] = (uint32_t)((int)rintf(ldexpf(widen2<DT>((uint32_t)(q4[2 * (w % 2) + k / 2] & keep))[k % 2], 22 - e)) + 0x808080);
             const uint32_t x = __builtin_amdgcn_perm(v[1], v[0], 0x05040100), y = __builtin_amdgcn_perm(v[3], v[2], 0x05040100);
-            parts[0][w] = (int)__builtin_amdgcn_perm(y, x, 0x07050301);
-            parts[1][w] = (int)(__builtin_amdgcn_perm(y, x, 0x06040200) ^ 0x80808080u);
+            q8[r][3 * i][w] = (int)((__builtin_amdgcn_perm(v[1], v[0], 0x0C0C0602) |
+                                     __builtin_amdgcn_perm(v[3], v[2], 0x06020C0C)) ^ 0x80808080u);
+            q8[r][3 * i + 1][w] = (int)(__builtin_amdgcn_perm(y, x, 0x07050301) ^ 0x80808080u);
+            q8[r][3 * i + 2][w] = (int)(__builtin_amdgcn_perm(y, x, 0x06040200) ^ 0x80808080u);
           }
-          qf[r][2 * i] = parts[0];
-          qf[r][2 * i + 1] = parts[1];
         }
       } else {
         // to [1, 2) by a power of two
@@ -339,33 +340,51 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
       vafter = page_of(j + 2 * STEP + vg);
     }
 
+    // The next tile's K in four places among this tile's softmax, its V among the products
+    // with V: a wave that asks for much at once waits until the unit has taken it in.
+    const uint8_t* kp = nullptr;
+    auto more_k = [&](int quarter) __attribute__((always_inline)) {
+      if constexpr (MORE) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = NT * quarter / 4; t < NT * (quarter + 1) / 4; ++t) load_k(kp, t);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
     // ---- scores
     b4f s[RT][NT];
     if constexpr (INT8) {
-      b4i x[RT][NT];
+      if constexpr (MORE) kp = k_at(j + STEP, knext);
+      b4i x[RT][NT], y[RT][NT];                    // of the two upper digits and of the last
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
+      for (int step = 0; step < 3; ++step) {
+        const int digit = step == 0 ? 0 : 3 - step;   // the last between the others, which wait for each other
+        if (digit == 1)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) x[r][t] <<= 8;   // at most 128 x 128 x 128 x 256 = 2^29
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              if (part == 0 && i == 0) x[r][t] = (b4i){0, 0, 0, 0};
-              x[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kw[t][i], qf[r][2 * i + part], x[r][t], 0, 0, 0);
+              b4i& to = digit < 2 ? x[r][t] : y[r][t];
+              if (digit != 1 && i == 0) to = (b4i){0, 0, 0, 0};
+              to = __builtin_amdgcn_mfma_i32_16x16x64_i8(kw[t][i], q8[r][3 * i + digit], to, 0, 0, 0);
             }
-        if (part == 0)
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) x[r][t] <<= 8;   // at most 128 x 127 x 128 x 256 < 2^30
       }
+      // K's first quarter before the sums are ready (after them 16 requests of up to 16384
+      // keys 78.0 us, so 67.1)
+      more_k(0);
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[r][t][i] = (float)x[r][t][i];
+          for (int i = 0; i < 4; ++i) s[r][t][i] = fmaf((float)x[r][t][i], 256.0f, (float)y[r][t][i]);
     } else {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
@@ -381,21 +400,10 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
 #pragma unroll
           for (int r = 0; r < RT; ++r) s[r][t] = mma16<FP16>(kf, qf[r][st], s[r][t]);
         }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (MORE) kp = k_at(j + STEP, knext);
+      more_k(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    // The next tile's K in four places among this tile's softmax, its V among the products
-    // with V: a wave that asks for much at once waits until the unit has taken it in.
-    const uint8_t* kp = nullptr;
-    auto more_k = [&](int quarter) __attribute__((always_inline)) {
-      if constexpr (MORE) {
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = NT * quarter / 4; t < NT * (quarter + 1) / 4; ++t) load_k(kp, t);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    };
-    if constexpr (MORE) kp = k_at(j + STEP, knext);
-    more_k(0);
     if constexpr (CODES) {
       if (lc < lo || lc >= hi) vs = 0.f;
       // room for V's scales

@@ -94,3 +94,21 @@ def test_large_values_written_by_the_writer():
         B.cache_write(cache, ints(table), ints(np.arange(100)), k, v, entry=ints(np.zeros(100)))
         o, lse = _gpu(q, cache, table, [100])
         _check(o, lse, qv, cache, table, [100], fmt, "bf16", 0.125, fmt)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("ratio", [1, 300, 3000, 30000])
+@pytest.mark.parametrize("heads", [6, 20])
+def test_query_channels_that_stand_out(fmt, kind, ratio, heads):
+    """One channel of the queries is many times the others', and the keys are small there in proportion: the scores come
+    from the others, and so do the output's bits.  Multiples of 1 / 64 below 4: 2^-22 of 2^16."""
+    D, page, T = 128, 64, 9
+    cache = random_cache(T, 1, page, D, fmt, kind, 231)
+    cache.k.view(torch.uint8)[..., 77] = 0
+    q = np.clip(np.round(np.random.default_rng(232).standard_normal((1, heads, D)) * 64) / 64, -3.5, 3.5)
+    q[..., 77] = ratio * np.where(q[..., 77] < 0, -1.9, 1.99)
+    q, qv = device(q, kind)
+    table = random_table(1, T, T, 233)
+    o, lse = _gpu(q, cache, table, [T * page - 3], scale=0.5)
+    _check(o, lse, qv, cache, table, [T * page - 3], fmt, kind, 0.5, f"ratio {ratio}", exact=True)
