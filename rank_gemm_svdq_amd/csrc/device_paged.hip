@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
   const int D = PAD ? c.D : DP;
   // ---- Q: asked for before all else
   b4i qf[RT][NS], q8[RT][INT8 ? 3 * NC : 1];     // (q8: INT8's digits)
-  float rq[RT], slope[RT];                       // a row's factor
+  float rq[RT], rk[RT], slope[RT];               // a row's factor, in two: at most 1, at least 1
   int qh[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
@@ -264,7 +264,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    rq[r] = 1.f;
+    rq[r] = rk[r] = 1.f;
     if constexpr (CODES) {
       // largest magnitude of the row, as bits: infinities and NaN are the largest
       typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
@@ -286,7 +286,8 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
         // digits: the output 0.2 to 2.5 % off where a channel of the query is 300 to 3000 times
         // the others and the keys' is small in proportion; 600 keys 8.0 us, not 8.2.)
         const int e = max((int)((__float_as_uint(mag) + 0x10000u) >> 23), 1) - 127;
-        rq[r] = odd ? __builtin_nanf("") : ldexpf(p.qmul, e - 22);
+        rq[r] = odd ? __builtin_nanf("") : ldexpf(p.qmul, min(e - 22, 0));
+        rk[r] = ldexpf(1.0f, max(e - 22, 0));
         const int keep = odd ? 0 : -1;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
@@ -307,7 +308,8 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
       } else {
         // to [1, 2) by a power of two
         const int e = max((int)(__float_as_uint(mag) >> 23), 1) - 127;
-        rq[r] = odd ? __builtin_nanf("") : __uint_as_float((uint32_t)(e + 127) << 23);
+        rq[r] = odd ? __builtin_nanf("") : __uint_as_float((uint32_t)(min(e, 0) + 127) << 23);
+        rk[r] = __uint_as_float((uint32_t)(max(e, 0) + 127) << 23);
         const float by = ldexpf(p.qmul, -e);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
@@ -428,8 +430,11 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
     for (int r = 0; r < RT; ++r) {
       // in powers of two; rounded here and not in the exponent's sum, so that the largest
       // of enormous scores is the maximum itself
+      // A query's small factor before the key's scale, its large one after: no step leaves
+      // fp32 unless the score does
       if constexpr (CODES)
-        each([&](auto x) { s[r][x / 4][x % 4] = s[r][x / 4][x % 4] * of_lane<x>(ks) * rq[r]; }, std::make_integer_sequence<int, KPL>{});
+        each([&](auto x) { s[r][x / 4][x % 4] = s[r][x / 4][x % 4] * rq[r] * of_lane<x>(ks) * rk[r]; },
+             std::make_integer_sequence<int, KPL>{});
       if (a.softcap > 0.f) {
         const PagedP p = again();
         if (p.a.softcap <= kSmallCap) {

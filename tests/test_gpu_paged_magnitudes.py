@@ -96,6 +96,21 @@ def test_large_values_written_by_the_writer():
         _check(o, lse, qv, cache, table, [100], fmt, "bf16", 0.125, fmt)
 
 
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("power", [-125, -118, -100, -30, -18, -9, 9, 18, 30, 100, 118])
+def test_large_keys_and_small_queries_and_the_other_way_round(fmt, power):
+    """Scores of ordinary size whose factors are near the ends of fp32."""
+    D, page, T = 64, 32, 5
+    cache = random_cache(T, 2, page, D, fmt, "bf16", 211)
+    for s in (cache.k_scale, cache.v_scale):
+        s.clamp_(min=2.0**-6, max=2.0**-4)
+    cache.k_scale.mul_(2.0**-power)
+    q, qv = device(np.random.default_rng(212).standard_normal((1, 6, D)) * 2.0**power, "bf16")
+    table = random_table(1, T, T, 213)
+    o, lse = _gpu(q, cache, table, [150])
+    _check(o, lse, qv, cache, table, [150], fmt, "bf16", D ** -0.5, f"2^{power}")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
 @pytest.mark.parametrize("ratio", [1, 300, 3000, 30000])
