@@ -603,9 +603,10 @@ typedef struct svdq_paged_attention_args {
  * 24 bits, the sign's with them, of their row's largest magnitude (SVDQ_KV_INT8: an
  * element is off by 2^-22.9 of it at most) or to fp16 scaled by a power of two
  * (SVDQ_KV_FP8: by 2^-25 of it); with either a query that holds an infinity or a NaN
- * gets NaN where it sees a key.  Weights are rounded to fp16 (SVDQ_KV_VALUES: to the call's
- * type) for the product with V, not for their sum.  The same call on the same inputs
- * gives the same bits.
+ * gets NaN where it sees a key.  Weights, over codes times V's scale, are rounded to
+ * fp16 (SVDQ_KV_VALUES: to the call's type) for the product with V, not for their sum:
+ * each is off by 2^-11 of itself (bf16: 2^-8), in fp16 by 2^-31 of the row's largest if
+ * that is more.  The same call on the same inputs gives the same bits.
  * ws: device, 256-byte aligned, svdq_paged_attention_workspace_bytes() bytes, or
  * NULL if that is 0; its contents before the call do not matter, and calls that
  * overlap in time need one each.

@@ -21,8 +21,10 @@
 // that brings its largest element to [1, 2): what falls below fp16's range is under
 // 2^-24 of that.  INT8 keys are multiplied as they are by queries of 24 bits in three digits
 // of 8, summed exactly in int32; INT8 values become fp16 of their bits (widen_codes).
-// The key's scale multiplies the score, and the value's scale the weight, as a multiple
-// of a power of two that all the wave's scales so far stay under.
+// The key's scale multiplies the score, and the value's scale the weight; of these
+// products a row's largest so far is kept between 2^6 and 2^14 by a power of two (iv), which
+// rises and falls with the maximum, so that neither a scale without weight nor a weight
+// without scale takes the bits of those that count.
 //
 // Softmax.  A row's maximum is raised when a tile exceeds it by more than kLag
 // (powers of two), which a vote of the wave finds out without exchanges; weights
@@ -63,8 +65,10 @@ struct PagedP {
 constexpr float kLag = 8.0f;
 // fp16 weights between 2^6 and 2^14 at the maximum: the smallest that keeps its bits
 // is 2^-20 of it, 2^-30 with half of them.  bf16: room for 2^20 of the largest values.
+// Codes: at most 1, so that a weight times any scale of V stays in fp32; to fp16 go these
+// products, with a range of their own.
 template <int FMT, int DT>
-constexpr float kLift = FMT == SVDQ_KV_VALUES && DT == SVDQ_BF16 ? -20.0f : 6.0f;
+constexpr float kLift = FMT != SVDQ_KV_VALUES ? -kLag : DT == SVDQ_BF16 ? -20.0f : 6.0f;
 
 // FP16: codes or fp16 values
 template <bool FP16>
@@ -210,13 +214,14 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
     return;
   }
 
-  float m[RT], l[RT], iv = 0x1p126f;             // iv: 1 / the power of two that V's scales stay under
+  float m[RT], l[RT], iv[RT];                    // iv: what weights times V's scales are multiplied by, at most 2^126
   b4f o[RT][ND], ow[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
     ow[r] = (b4f){0.f, 0.f, 0.f, 0.f};
     m[r] = kLow;
     l[r] = 0.f;
+    iv[r] = 0x1p126f;
 #pragma unroll
     for (int d = 0; d < ND; ++d) o[r][d] = (b4f){0.f, 0.f, 0.f, 0.f};
   }
@@ -406,24 +411,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
       if constexpr (MORE) kp = k_at(j + STEP, knext);
       more_k(0);
     }
-    if constexpr (CODES) {
-      if (lc < lo || lc >= hi) vs = 0.f;
-      // room for V's scales
-      float big = vs;
-      if (__any(big * iv > 1.0f)) {
-        for (int d = 32; d; d >>= 1) big = fmaxf(big, __shfl_xor(big, d));
-        const int e = min(max((int)(__float_as_uint(big) >> 23) - 126, -126), 126);   // big < 2^e
-        const float next = __uint_as_float((uint32_t)(127 - e) << 23);
-        const float f = next * (1.0f / iv);   // (iv is a power of two: exact, or 0)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          ow[r] *= f;
-#pragma unroll
-          for (int d = 0; d < ND; ++d) o[r][d] *= f;
-        }
-        iv = next;
-      }
-    }
+    if (CODES && (lc < lo || lc >= hi)) vs = 0.f;
     more_k(1);
     b4i pf[RT][NU];
 #pragma unroll
@@ -475,14 +463,29 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, s[r][t][i]);
-      if (__any(top > m[r] + (LIFT + kLag))) {
-        const float up = fmaxf(m[r], row_max(top) - LIFT);
-        const float f = exp2_(m[r] - up);
-        m[r] = up;
-        l[r] *= f;
+      auto rescale = [&](float f) __attribute__((always_inline)) {
         ow[r] *= f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[r][d] *= f;
+      };
+      if (__any(top > m[r] + (LIFT + kLag))) {
+        if constexpr (CODES) {
+          // a whole number: by powers of two l falls and iv rises, as far as it may, in whose
+          // place the sums fall
+          const float up = fmaxf(m[r], floorf(row_max(top) - LIFT));
+          const int k = (int)fminf(up - m[r], 300.0f);
+          const float f = ldexpf(1.0f, -k), rise = fminf(ldexpf(1.0f, k), fminf(0x1p126f / iv[r], 0x1p126f));
+          m[r] = up;
+          l[r] *= f;
+          iv[r] *= rise;
+          if (__any(f * rise != 1.0f)) rescale(f * rise);
+        } else {
+          const float up = fmaxf(m[r], row_max(top) - LIFT);
+          const float f = exp2_(m[r] - up);
+          m[r] = up;
+          l[r] *= f;
+          rescale(f);
+        }
       }
       if (r == 0) more_k(3);
       float w[4 * NT];
@@ -492,8 +495,17 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
         l[r] += w[x];
       }
       if constexpr (CODES) {
-        const float by = vs * iv;
-        each([&](auto x) { w[x] *= of_lane<x>(by); }, std::make_integer_sequence<int, KPL>{});
+        float big = 0.f;
+        each([&](auto x) { big = fmaxf(big, w[x] *= of_lane<x>(vs)); }, std::make_integer_sequence<int, KPL>{});
+        if (__any(big * iv[r] > 0x1p14f)) {
+          big = row_max(big);
+          // the largest to [2^6, 2^7)
+          const float next = fminf(iv[r], ldexpf(1.0f, 133 - (int)(__float_as_uint(big) >> 23)));
+          rescale(next * (1.0f / iv[r]));   // (powers of two: exact, or 0)
+          iv[r] = next;
+        }
+#pragma unroll
+        for (int x = 0; x < 4 * NT; ++x) w[x] *= iv[r];
       }
       // To the product with V the weights go in 16 bits, as the matrix unit takes them
 #pragma unroll
@@ -567,7 +579,7 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
     const float sum = row_sum(l[r]);
     // a mean of codes is at most 448, so the scale comes back after the division; INT8's
     // 2^24 with the division, as together with the scale it may leave fp32
-    const float by = sum != 0.f ? (INT8 ? 0x1p24f : 1.0f) / sum : 0.f, back = CODES ? 1.0f / iv : 1.f;
+    const float by = sum != 0.f ? (INT8 ? 0x1p24f : 1.0f) / sum : 0.f, back = CODES ? 1.0f / iv[r] : 1.f;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
       *reinterpret_cast<b4f*>(&jo[wave][16 * r + lc][16 * d + 4 * lu]) =

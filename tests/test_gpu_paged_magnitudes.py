@@ -111,6 +111,54 @@ def test_large_keys_and_small_queries_and_the_other_way_round(fmt, power):
     _check(o, lse, qv, cache, table, [150], fmt, "bf16", D ** -0.5, f"2^{power}")
 
 
+def _laid(z, s, fmt, kind, seed):
+    """A cache of one head whose key j scores z[j] against the first unit vector and has value scale s[j]."""
+    D, page = 64, 32
+    T = -(-len(z) // page)
+    cache = random_cache(T, 1, page, D, fmt, kind, seed)
+    cache.k.view(torch.uint8).zero_()
+    cache.k_scale.fill_(1.0)
+    put = lambda a: torch.from_numpy(np.resize(a, T * page).astype(np.float32)).view(T, 1, page).cuda()
+    cache.k.view(torch.uint8)[:, :, :, 0] = put(z).to(cache.k.dtype).view(torch.uint8)
+    cache.v_scale.copy_(put(s))
+    q = torch.zeros((1, 3, D), dtype=torch.bfloat16 if kind == "bf16" else torch.float16, device="cuda")
+    q[0, :, 0] = torch.tensor([1.0, 0.5, 0.25])
+    return cache, q, np.arange(T)[None].astype(np.int32)
+
+
+@pytest.mark.parametrize("fmt,kind", [("int8", "bf16"), ("int8", "fp16"), ("fp8", "bf16"), ("fp8", "fp16")])
+@pytest.mark.parametrize("gap", [8, 20, 24, 31, 60])
+@pytest.mark.parametrize("n", [40, 600, 2100])
+def test_large_values_of_little_weight(fmt, kind, gap, n):
+    """A few keys of next to no weight have values 2^gap times the others': the others keep their bits, wherever it lies."""
+    rng = np.random.default_rng(gap)
+    for at in (0, 17, n // 2, n - 1):
+        z, s = rng.integers(-2, 3, n).astype(float), rng.uniform(0.5, 1.0, n) * 2.0**-10
+        z[at], s[at] = -100.0 * (1 if gap > 8 else 0.5), 2.0**(gap - 10)
+        if fmt == "fp8":
+            z[at] = -96.0
+            s = np.exp2(np.round(np.log2(s)))
+        cache, q, table = _laid(z, s, fmt, kind, 221)
+        q = q[:, :2]
+        o, lse = _gpu(q, cache, table, [n], scale=1.0)
+        _check(o, lse, values(q), cache, table, [n], fmt, kind, 1.0, f"gap {gap} at {at}")
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8"])
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("n", [64, 500, 3000])
+def test_products_of_weight_and_value_of_one_size(fmt, order, n):
+    """Weights and values' scales each over many powers of two, their products of like size: all of them count."""
+    z = np.linspace(-36, 36, n).round()
+    if fmt == "fp8":
+        z = 4 * (z / 4).round()                        # E4M3 holds these
+    s = np.exp2(np.round(-z * 1.4427))
+    i = {"rising": slice(None), "falling": slice(None, None, -1), "mixed": np.random.default_rng(222).permutation(n)}[order]
+    cache, q, table = _laid(z[i], s[i], fmt, "bf16", 223)
+    o, lse = _gpu(q, cache, table, [n], scale=1.0)
+    _check(o, lse, values(q), cache, table, [n], fmt, "bf16", 1.0, order)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
 @pytest.mark.parametrize("ratio", [1, 300, 3000, 30000])
