@@ -1,12 +1,13 @@
-"""Attention over 8-bit pages where scales, queries and values are of very different size, against the 64-bit oracle.
+"""Attention over pages, mostly of 8 bits, where scales, queries and values are of very different size, against the
+64-bit oracle.
 
 Bound.  With u = 2^-24, p a key's weight of sum 1, V its largest |v| and n the keys seen:
   score   (2 D + 16) u times its magnitudes, and what the query loses: E4M3 2^-25 of the row's largest element (half of
           fp16's smallest step at [1, 2)), INT8 half a step of 2^-22 of a power of two that the largest is at least
           0.996 of, 2^-22.9 of the largest, each times sum |k|;
   weight  e^2d - 1 < 3 d relative, d that error and 2^-21 for the exponential, on mean |v| + |o|;
-  to fp16 2^-11 of each term, and 2^-25 absolute where the largest product p V / (127 or 224) is held above 2^6: 2^-31
-          of it a key, times codes of at most 127 or 448: n 2^-30 max (p V);
+  to 16 bits 2^-11 of each term (bf16 values 2^-8), and over codes 2^-25 absolute where the largest product
+          p V / (127 or 224) is held above 2^6: 2^-31 of it a key, times codes of at most 127 or 448: n 2^-30 max (p V);
   sums    (2 n + 16) u of mean |v| + |o|; INT8 values are summed as code + 128 <= 255 and 128 times the weights taken out:
           2 n u of at most 3 sum p V.
 The store adds half an ulp.  The logarithm of the sum is off by d + 2 n u, 2^-17 and 2^-22 of itself."""
@@ -44,10 +45,12 @@ def _bounds(qv, nc, table, kv_len, fmt, scale, exact=False):
             z = scale * (k[b, :kv_len[b], h // G] @ qv[b, h])
             pv = np.exp(z - ls[b, h]) * np.abs(v[b, :kv_len[b], h // G]).max(-1)
             most[b, h], total[b, h] = pv.max(), pv.sum()
-    lost = 0.0 if exact else 2.0**-22.9 if fmt == "int8" else 2.0**-25
+    lost = 0.0 if exact or fmt == "values" else 2.0**-22.9 if fmt == "int8" else 2.0**-25
     d = (2 * D + 16) * U * weight + 2.0**-21 + lost * np.abs(qv).max(-1) * abs(scale) * np.abs(k).sum(-1).max()
     n = seen[..., None]
-    e = (3 * d[..., None] + 2.0**-11 + (2 * n + 16) * U) * (mean + np.abs(want)) + n * 2.0**-30 * most[..., None]
+    e = (3 * d[..., None] + (2.0**-8 if fmt == "values" else 2.0**-11) + (2 * n + 16) * U) * (mean + np.abs(want))
+    if fmt != "values":
+        e = e + n * 2.0**-30 * most[..., None]
     if fmt == "int8":
         e = e + 6 * n * U * total[..., None]
     return want, e, ls, d + 2 * seen * U + 2.0**-17 + 2.0**-22 * np.abs(ls)
@@ -80,6 +83,23 @@ def test_values_near_the_end_of_the_type(fmt, low, high, order):
             got = values(o)
             assert not np.isnan(got).any() and np.isinf(got[np.abs(want) - e >= 65520]).all()
             assert fmt == "int8" or (got[want == 0] == 0).all()      # (INT8: a difference of sums)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "values"])
+def test_values_near_the_end_of_the_type_in_parts(fmt):
+    """Enough keys that blocks share them and their means are joined."""
+    D, page, T = 64, 64, 64
+    cache = random_cache(T, 2, page, D, fmt, "bf16", 205)
+    if fmt == "values":
+        cache.v.uniform_(-1e38, 1e38)
+    else:
+        cache.v_scale.fill_(2.0**118)
+    table = random_table(1, T, T, 206)
+    q, qv = device(np.random.default_rng(207).standard_normal((1, 4, D)), "bf16")
+    assert B.paged_attention_workspace_bytes(cache, 1, T, 4) > 0
+    for n in (T * page, 1000):
+        o, lse = _gpu(q, cache, table, [n])
+        _check(o, lse, qv, cache, table, [n], fmt, "bf16", D ** -0.5, f"{fmt} {n}")
 
 
 def test_large_values_written_by_the_writer():
