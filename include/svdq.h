@@ -607,6 +607,10 @@ typedef struct svdq_paged_attention_args {
  * fp16 (SVDQ_KV_VALUES: to the call's type) for the product with V, not for their sum:
  * each is off by 2^-11 of itself (bf16: 2^-8), in fp16 by 2^-31 of the row's largest if
  * that is more.  The same call on the same inputs gives the same bits.
+ * A request's keys are shared among blocks by the table's width T (and the window), not
+ * by kv_len, which lies on the device: a table several times wider than the lengths in
+ * use costs time (4096 keys of 8 heads of 128 take 10 us with T page = 4096, 29 with
+ * 131072).  T may be less than the rows' length: table_row is their distance.
  * ws: device, 256-byte aligned, svdq_paged_attention_workspace_bytes() bytes, or
  * NULL if that is 0; its contents before the call do not matter, and calls that
  * overlap in time need one each.

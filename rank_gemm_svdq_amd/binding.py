@@ -707,8 +707,8 @@ class KVCache:
     bfloat16, float16 or int16 (bf16 bits) values without.  A page's own elements
     are contiguous; pages may be any distance apart.  page: 16, 32, .. 256; D a
     multiple of 16 up to 128.  The cache goes on using these tensors' memory: they
-    are not to be resized, and another tensor takes a new KVCache.  A copy has copies
-    of them."""
+    are not to be resized, and another tensor takes a new KVCache.  A deep copy has copies
+    of them, copy.copy() the same ones."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
         self._tensors = k, v, k_scale, v_scale
@@ -766,7 +766,9 @@ def paged_attention(q, cache, table, kv_len, o, ws, scale=None, softcap=0.0, win
     request, q, o [B, Hq, D], over the kv_len[b] keys (its own among them) in
     the pages table[b]; ws from paged_attention_workspace().  scale: D ** -0.5 if
     None.  window: only the last so many keys (0: all).  slopes [Hq], lse
-    [B, Hq] float32; table [B, T], kv_len [B] int32."""
+    [B, Hq] float32; table [B, T], kv_len [B] int32.  The keys are shared among blocks by T,
+    so a table of the first columns that the longest request needs, table[:, :n], with a
+    workspace of its own, takes less time than one for far more."""
     (_blk or _block()).paged_attention(cache.handle, q, table, kv_len, o, ws, scale, softcap, window, slopes, lse, stream)
 
 

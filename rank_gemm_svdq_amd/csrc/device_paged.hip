@@ -32,13 +32,17 @@
 //
 // What bounds it.  Each key and value is read once, and the memory's rate is reached where
 // all compute units have work: 16 requests of up to 16384 INT8 keys, 8 heads of 128,
-// 66.7 us; one of 131072 E4M3 keys 54.1; 40 of up to 3001 fp16 keys within a window of
-// 1500, 24 heads of 64, 63.5.  A compute unit by itself takes in 27 GB/s from memory and 46
-// from the last-level cache, however many waves ask, so fewer blocks than units leave the
-// rate behind; 600 INT8 keys take 9.1 us, which is two launches and the chain
-// length, page, K, scores, V, join.  (Blocks of eight waves, a
-// wave on two tiles at a time, K in whole lines with its pieces exchanged: the same time;
-// K and V loaded past the caches: 5 to 10 % more.)
+// 67.1 us; one of 131072 E4M3 keys 54.4; 40 of up to 3001 fp16 keys within a window of
+// 1500, 24 heads of 64, 63.5.  A compute unit by itself takes in 49 GB/s where eight do and
+// 42 where 128 do, from memory and from the last-level cache alike, however many waves ask,
+// so fewer blocks than units leave the rate behind; 600 INT8 keys take 8.2 us in one part,
+// which is a launch and the chain length, page, K, scores, V, join of waves.  (Blocks of
+// eight waves, a wave on two tiles at a time, K in whole lines with its pieces exchanged: the
+// same time; K and V loaded past the caches: 5 to 10 % more.)
+//
+// Parts are shares of the table's width, which the host sees, not of the lengths: 4096 keys
+// take 10.0 us in a table for as many and 28.9 in one for 131072; 15 requests of 512 keys
+// beside one of 131072 take 356.
 #include "device_kv.h"
 #include "device_score.h"
 
@@ -64,7 +68,8 @@ struct PagedP {
 
 constexpr float kLag = 8.0f;
 // fp16 weights between 2^6 and 2^14 at the maximum: the smallest that keeps its bits
-// is 2^-20 of it, 2^-30 with half of them.  bf16: room for 2^20 of the largest values.
+// is 2^-20 of it, 2^-30 with half of them.  bf16: room for 2^12 of the largest values in a
+// wave's sum, for 2^20 at the weight that the maximum was taken from.
 // Codes: at most 1, so that a weight times any scale of V stays in fp32; to fp16 go these
 // products, with a range of their own.
 template <int FMT, int DT>
@@ -713,16 +718,17 @@ struct PagedPlan {
 // Parts of a row of keys by the least time, in ns.  A compute unit brings in what the four
 // tiles of a block's step need (heads of 128) in 1490 where few blocks run, 2090 where 128
 // do (what it can have under way at a time bounds it, and a second block beside the first
-// does not help), or all of them at the rate of the memory, of which a batch's
-// lengths leave about 0.7 in use; so blocks are as many to a compute unit as the fullest
-// has.  Start and end are 4500, 700 more for each block after the first, and the join
+// does not help), or all of them at the rate of the memory.  A batch is priced at 0.7 of
+// its table, the mean where lengths lie evenly between two fifths of it and all, as the host does
+// not see them (one of equal lengths costs 1.4 times that).  Blocks are as many to a
+// compute unit as the fullest has.  Start and end are 4500, 700 more for each block after the first, and the join
 // 3900, 100 a part up to 16 and 8 a part.
-// (us in 1, 2, 4, 8, 16, 32 parts, 8 K/V heads of 128, codes: 640 keys 9.9, 11.8, 11.3 from
-// memory and 8.3, 9.9, 9.0 from the last-level cache; 4096 keys 24.8, 16.9, 12.3, 11.0,
-// 9.9, 9.8; 16384 88, 49, 28.6, 18.4, 13.9, 12.9; 131072 986, 501, 258, 137, 78, 54.1, in 48
-// 64.2; 16 requests of up to 16384 in 1, 2, 3, 4 98.1, 67.0, 83.7, 69.9; 64 of 1024 19.0, 24.6,
-// 24.6; 40 of 4096 58.2, 53.6, 55.2, 52.5.  A dearer join costs single long requests, a
-// cheaper one batches of some hundred keys: 16 of 1280 14.7 in one part, 16.1 in two.)
+// (us in 1, 2, 4, 8, 16, 32 parts, 8 K/V heads of 128, INT8: 600 keys 8.3, 10.2, 9.2, the
+// same beyond; 4096 keys 25.0, 17.8, 12.6, 10.8, 10.1, 10.2; 16384 88, 49, 28.9, 18.7, 13.9,
+// 12.8; 131072 704, 360, 187, 102, 61.6, 53.6, in 48 59.8; 16 requests of up to 16384 in 1,
+// 2, 3, 4 97.5, 67.2, 84.1, 70.3; 64 of 1024 19.4, 25.0, 24.9, 32.7; 40 of 4096 58.4, 54.1, 55.5,
+// 52.8.  A dearer join costs single long requests, a cheaper one batches of some hundred
+// keys: 16 of 1280 11.4 in one part, 12.8 in two.)
 PagedPlan plan_of(const svdq_kv_cache& c, int32_t B, int64_t keys, int32_t Hq) {
   PagedPlan p;
   p.G = Hq / c.heads;
