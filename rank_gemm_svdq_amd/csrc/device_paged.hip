@@ -68,12 +68,12 @@ struct PagedP {
 
 constexpr float kLag = 8.0f;
 // fp16 weights between 2^6 and 2^14 at the maximum: the smallest that keeps its bits
-// is 2^-20 of it, 2^-30 with half of them.  bf16: room for 2^12 of the largest values in a
-// wave's sum, for 2^20 at the weight that the maximum was taken from.
+// is 2^-20 of it, 2^-30 with half of them.  bf16: at most 2^-22, so that the sum of the 2^22
+// keys that a wave may see stays in fp32 whatever their values (those under 2^-96 lose bits).
 // Codes: at most 1, so that a weight times any scale of V stays in fp32; to fp16 go these
 // products, with a range of their own.
 template <int FMT, int DT>
-constexpr float kLift = FMT != SVDQ_KV_VALUES ? -kLag : DT == SVDQ_BF16 ? -20.0f : 6.0f;
+constexpr float kLift = FMT != SVDQ_KV_VALUES ? -kLag : DT == SVDQ_BF16 ? -30.0f : 6.0f;
 
 // FP16: codes or fp16 values
 template <bool FP16>
@@ -421,13 +421,13 @@ __global__ __launch_bounds__(256, RT == 2 && DP == 128 ? 1 : 2) void paged_kerne
     b4i pf[RT][NU];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      // in powers of two; rounded here and not in the exponent's sum, so that the largest
-      // of enormous scores is the maximum itself
-      // A query's small factor before the key's scale, its large one after: no step leaves
-      // fp32 unless the score does
+      // a query's small factor before the key's scale, its large one after: no step leaves
+      // fp32 unless q.k does
       if constexpr (CODES)
         each([&](auto x) { s[r][x / 4][x % 4] = s[r][x / 4][x % 4] * rq[r] * of_lane<x>(ks) * rk[r]; },
              std::make_integer_sequence<int, KPL>{});
+      // in powers of two; rounded here and not in the exponent's sum, so that the largest
+      // of enormous scores is the maximum itself
       if (a.softcap > 0.f) {
         const PagedP p = again();
         if (p.a.softcap <= kSmallCap) {

@@ -102,6 +102,32 @@ def test_values_near_the_end_of_the_type_in_parts(fmt):
         _check(o, lse, qv, cache, table, [n], fmt, "bf16", D ** -0.5, f"{fmt} {n}")
 
 
+@pytest.mark.parametrize("fmt", ["int8", "fp8", "values"])
+def test_sums_of_many_large_values(fmt):
+    """32768 keys to a wave, all of like weight after a first tile of less, every value the same near the end of bf16: the
+    output is that value, off by the weights' rounding (2^-8 at most for bf16), the sums' and the store's."""
+    D, page, T, requests = 64, 256, 512, 64
+    cache = random_cache(T, 8, page, D, fmt, "bf16", 208)
+    cache.k.view(torch.uint8).zero_()
+    cache.k[:, :, :, 0] = torch.full((T, 8, page), 4.0, device="cuda").to(cache.k.dtype)
+    cache.k[:2, :, :, 0] = torch.full((2, 8, page), -1.0, device="cuda").to(cache.k.dtype)      # weight e^-5, 2^-7.2
+    if fmt == "values":
+        cache.v.fill_(1e38)
+        v = float(cache.v[0, 0, 0, 0])
+    else:
+        cache.k_scale.fill_(1.0)
+        cache.v.copy_(torch.full(cache.v.shape, 112.0).to(cache.v.dtype))
+        cache.v_scale.fill_(2.0**119)
+        v = 112.0 * 2.0**119
+    q = torch.zeros((requests, 8, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    table = np.tile(np.arange(T), (requests, 1))       # the requests share their pages
+    assert B.paged_attention_workspace_bytes(cache, requests, T, 8) == 0
+    o, _ = _gpu(q, cache, table, [T * page] * requests, scale=1.0)
+    e = v * (2.0**-8 + (2 * T * page + 16) * U * (3 if fmt == "int8" else 1))
+    assert_within(values(o), np.full(q.shape, v), e + half_ulp(np.full(q.shape, v), "bf16"), fmt)
+
+
 def test_large_values_written_by_the_writer():
     """Values of 1e34 to 1e38 through the whole path."""
     rng = np.random.default_rng(203)
